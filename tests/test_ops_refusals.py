@@ -1,0 +1,271 @@
+"""The row norm's and the gradient list's entry points on a host without a GPU: every declared
+symbol is exported, invalid arguments are refused with the documented status before anything
+touches the device, and the binding refuses tensors of the wrong sizes, dtypes or layouts."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import unet_groupnorm_amd as gn
+from unet_groupnorm_amd._lib import GN_BF16, GN_F16, GN_F32, OPS_STATUS_NAMES, GnGradTensor, lib
+from unet_groupnorm_amd.gn import GnError
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "gn_ops.h")
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def at(k):
+    """A fake aligned address; the checks below never look behind it. 1 MiB apart."""
+    return ctypes.c_void_p(0x10000000 + (k << 20))
+
+
+def test_every_declared_function_is_exported():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"^\s*(?:const\s+)?[a-z_0-9]+\s*\*?\s*(gn_[a-z_0-9]+)\s*\(", text, flags=re.M))
+    assert len(names) == 9, names
+    for name in names:
+        assert hasattr(lib, name), name
+
+
+def test_status_names_match_the_header():
+    text = open(HEADER).read()
+    for code, name in OPS_STATUS_NAMES.items():
+        assert re.search(rf"\b{name}\s*=\s*{code}\b", text), name
+        assert lib.gn_ops_status_string(code) != b"unknown status"
+    assert lib.gn_ops_status_string(0) == b"ok" and lib.gn_ops_status_string(999) == b"unknown status"
+
+
+def test_gradient_record_matches_the_header():
+    text = open(HEADER).read()
+    body = re.search(r"typedef struct gn_grad_tensor \{(.*?)\} gn_grad_tensor;", text, re.S).group(1)
+    names = [d.split()[-1].lstrip("*") for d in body.split(";") if d.strip()]
+    assert names == [n for n, _ in GnGradTensor._fields_] and ctypes.sizeof(GnGradTensor) == 32
+
+
+def fwd(**kw):
+    a = dict(x=at(0), xdt=GN_BF16, xs=64, res=None, rdt=GN_BF16, w=at(1), wdt=GN_BF16, T=4, H=64, eps=1e-6, y=at(2),
+             ydt=GN_BF16, h=None, rstd=at(3), stream=None)
+    a.update(kw)
+    return lib.gn_rms_forward(*a.values())
+
+
+RES = dict(res=at(4), h=at(5))
+FWD_BAD = [
+    (dict(x=None), 1), (dict(y=None), 1), (dict(res=at(4)), 1), (dict(h=at(4)), 1),
+    (dict(T=-1), 32), (dict(H=0), 32), (dict(H=32769, xs=32769), 32), (dict(xs=63), 32), (dict(T=1 << 45), 32),
+    (dict(xdt=3), 4), (dict(wdt=GN_F16), 4), (dict(ydt=GN_F16), 4), (dict(**RES, rdt=GN_F16), 4),
+    (dict(xdt=GN_F32, wdt=GN_F32, ydt=GN_BF16), 4),
+    (dict(eps=-1e-6), 5), (dict(eps=float("nan")), 5), (dict(eps=float("inf")), 5),
+    (dict(x=ctypes.c_void_p(0x10000001)), 7), (dict(rstd=ctypes.c_void_p(0x10300002)), 7),
+    (dict(w=at(1), wdt=GN_F32, y=ctypes.c_void_p(0x10200001)), 7),
+    (dict(y=ctypes.c_void_p(0x10000002)), 33),            # y shifted into x
+    (dict(y=at(0), xs=128), 33),                          # in place over strided rows
+    (dict(y=at(0), ydt=GN_F32), 33),                      # in place in a wider type
+    (dict(y=at(1)), 33), (dict(rstd=at(0)), 33), (dict(rstd=at(1)), 33),
+    (dict(res=at(4), h=ctypes.c_void_p(0x10400002)), 33), (dict(res=at(4), h=at(0)), 33), (dict(res=at(4), h=at(2)), 33),
+]
+
+
+@pytest.mark.parametrize("kw,status", FWD_BAD, ids=str)
+def test_forward_refusals(kw, status):
+    assert fwd(**kw) == status
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(y=at(0)), dict(**RES), dict(res=at(4), h=at(4)), dict(w=None),
+                                dict(xs=1000), dict(rstd=None)], ids=str)
+def test_forward_good_arguments_reach_the_device_check(kw):
+    assert fwd(**kw) == 8
+
+
+def test_no_rows_is_a_call_that_does_nothing():
+    assert fwd(T=0, x=None, y=None) == 0
+    assert lib.gn_q8_dequantize(None, 0, None, 0, 64, 0, None, GN_F32, None) == 0
+
+
+def q8(**kw):
+    a = dict(x=at(0), xdt=GN_BF16, xs=64, res=None, rdt=GN_BF16, w=at(1), wdt=GN_BF16, T=4, H=64, eps=1e-6, block=0,
+             q=at(2), qdt=0, scale=at(3), h=None, rstd=None, stream=None)
+    a.update(kw)
+    return lib.gn_rms_forward_q8(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), 1), (dict(scale=None), 1), (dict(qdt=2), 4), (dict(qdt=-1), 4), (dict(block=16), 34),
+    (dict(block=-32), 34), (dict(q=at(0)), 33), (dict(scale=at(2)), 33), (dict(scale=at(0)), 33), (dict(xs=1), 32),
+    (dict(scale=ctypes.c_void_p(0x10300001)), 7), (dict(), 8), (dict(block=128), 8),
+], ids=str)
+def test_q8_refusals(kw, status):
+    assert q8(**kw) == status
+
+
+def test_dequantize_refusals():
+    def call(q=at(0), qdt=0, s=at(1), T=4, H=64, block=0, o=at(2), odt=GN_F32):
+        return lib.gn_q8_dequantize(q, qdt, s, T, H, block, o, odt, None)
+    assert call(q=None) == 1 and call(s=None) == 1 and call(o=None) == 1
+    assert call(qdt=5) == 4 and call(odt=9) == 4 and call(block=8) == 34 and call(H=0) == 32
+    assert call(o=at(0)) == 33 and call(o=at(1)) == 33 and call(s=ctypes.c_void_p(0x10100001)) == 7 and call() == 8
+
+
+def bwd(**kw):
+    a = dict(dy=at(0), dydt=GN_BF16, h=at(1), hdt=GN_BF16, hs=64, rstd=at(2), w=at(3), wdt=GN_BF16, dh=None, T=4, H=64,
+             dx=at(4), xdt=GN_BF16, dres=None, dw=at(5), ws=at(6), wsb=1 << 20, stream=None)
+    a.update(kw)
+    return lib.gn_rms_backward(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dy=None), 1), (dict(h=None), 1), (dict(rstd=None), 1), (dict(dx=None, dw=None), 1), (dict(ws=None), 1),
+    (dict(H=0), 32), (dict(hs=63), 32), (dict(T=-1), 32),
+    (dict(xdt=GN_F16), 4), (dict(dydt=GN_F16), 4), (dict(wdt=GN_F16), 4), (dict(hdt=7), 4), (dict(w=None, wdt=GN_F16), 4),
+    (dict(wsb=16), 6), (dict(ws=ctypes.c_void_p(0x10600004)), 7), (dict(dx=ctypes.c_void_p(0x10400001)), 7),
+    (dict(dx=ctypes.c_void_p(0x10000002)), 33), (dict(dx=at(1), hs=128), 33), (dict(dx=at(3)), 33),
+    (dict(dres=at(4)), 33), (dict(dw=at(0)), 33), (dict(ws=at(0)), 33), (dict(dx=at(6)), 33),
+    (dict(), 8), (dict(dx=at(0)), 8), (dict(dx=at(1)), 8), (dict(dh=at(7), dx=at(7)), 8), (dict(dw=None, ws=None, wsb=0), 8),
+    (dict(hdt=GN_F32, dres=at(7)), 8), (dict(T=0, dw=None, ws=None), 0),
+], ids=str)
+def test_backward_refusals(kw, status):
+    assert bwd(**kw) == status
+
+
+def test_workspace_queries():
+    assert lib.gn_rms_workspace_bytes(-1, 64) == 0 and lib.gn_rms_workspace_bytes(4, 32769) == 0
+    assert 0 < lib.gn_rms_workspace_bytes(0, 64) <= lib.gn_rms_workspace_bytes(1 << 20, 64) <= 4096 * 64 * 4
+    assert lib.gn_grad_workspace_bytes(None, 1) == 0
+    assert gn.gn_grad_workspace_bytes([torch.zeros(5)]) == 8
+    assert gn.gn_grad_workspace_bytes([torch.zeros(0)]) == 8
+    many = [torch.zeros(1)] * 400       # three tables
+    assert gn.gn_grad_workspace_bytes(many) == 400 * 8
+
+
+def glist(*rows):
+    arr = (GnGradTensor * len(rows))()
+    for a, (d, o, n, dt, odt) in zip(arr, rows):
+        a.data, a.out, a.numel, a.dtype, a.out_dtype = d.value if d else None, o.value if o else None, n, dt, odt
+    return arr
+
+
+@pytest.mark.parametrize("rows,status", [
+    ([(at(0), at(1), -1, 0, 0)], 32), ([(None, at(1), 4, 0, 0)], 1), ([(at(0), None, 4, 0, 0)], 1),
+    ([(at(0), at(1), 4, 5, 0)], 4), ([(at(0), at(1), 4, GN_BF16, GN_F16)], 4), ([(at(0), at(1), 4, GN_F32, GN_BF16)], 4),
+    ([(ctypes.c_void_p(0x10000002), at(1), 4, 0, 0)], 7),
+    ([(at(0), at(0), 4, 0, 0), (at(0), at(0), 4, 0, 0)], 33),                    # the same tensor twice
+    ([(at(0), at(1), 4, 0, 0), (at(2), at(1), 4, 0, 0)], 33),                    # one output for two
+    ([(at(0), at(2), 4, 0, 0), (at(2), at(3), 4, 0, 0)], 33),                    # an output over another's data
+    ([(at(0), at(0), 4, GN_BF16, GN_F32)], 33),                                  # in place in a wider type
+    ([(at(0), at(8), 4, 0, 0)], 33), ([(at(9), at(1), 4, 0, 0)], 33),            # over the norm, from the workspace
+    ([(at(0), at(0), 4, 0, 0), (at(1), at(1), 4, 1, 1), (None, None, 0, 0, 0)], 8),
+    ([(at(3), at(3), 4, 0, 0), (at(1), at(2), 4, 1, 0)], 8),
+], ids=str)
+def test_clip_refusals(rows, status):
+    assert lib.gn_grad_clip(glist(*rows), len(rows), 0, 1.0, at(8), at(9), 1 << 16, None) == status
+
+
+def test_norm_refusals():
+    t = glist((at(0), None, 4, 0, 0), (at(0), None, 4, 0, 0))       # twice: counted twice, not refused
+    assert lib.gn_grad_norm(t, 2, 0, at(8), at(9), 1 << 16, None) == 8
+    assert lib.gn_grad_norm(t, 0, 0, at(8), at(9), 1 << 16, None) == 32
+    assert lib.gn_grad_norm(None, 1, 0, at(8), at(9), 1 << 16, None) == 1
+    assert lib.gn_grad_norm(t, 2, 2, at(8), at(9), 1 << 16, None) == 35
+    assert lib.gn_grad_norm(t, 2, 0, None, at(9), 1 << 16, None) == 1
+    assert lib.gn_grad_norm(t, 2, 0, at(8), None, 1 << 16, None) == 1
+    assert lib.gn_grad_norm(t, 2, 0, at(8), at(9), 8, None) == 6
+    assert lib.gn_grad_norm(t, 2, 0, at(9), at(9), 1 << 16, None) == 33
+    assert lib.gn_grad_norm(t, 2, 0, at(8), ctypes.c_void_p(0x10900008), 1 << 16, None) == 7
+    t = glist((at(0), at(1), 4, 0, 0))
+    for bad in (-1.0, float("nan")):
+        assert lib.gn_grad_clip(t, 1, 0, bad, at(8), at(9), 1 << 16, None) == 35
+
+
+# ------------------------------------------------------------------ the binding
+
+def _x(dtype=BF, shape=(3, 5, 64)):
+    return torch.ones(shape, dtype=dtype)
+
+
+def test_calls_reach_the_library_when_every_tensor_is_right():
+    x, w = _x(), torch.ones(64)
+    for call in (lambda: gn.gn_rms_forward(x, w, residual=_x(F32)),
+                 lambda: gn.gn_rms_forward_q8(x, w, block=32),
+                 lambda: gn.gn_q8_dequantize(_x(torch.int8), torch.ones(3, 5, 1)),
+                 lambda: gn.gn_rms_backward(x, _x(F32), torch.ones(3, 5), w, x_dtype=BF),
+                 lambda: gn.gn_grad_norm([x, w]), lambda: gn.gn_grad_clip([x, w], 1.0),
+                 lambda: gn.rms_norm(x[..., :32], None)):
+        with pytest.raises(GnError) as e:
+            call()
+        assert e.value.status == 8 and "GN_ERR_DEVICE" in str(e.value)
+
+
+@pytest.mark.parametrize("kw,err", [
+    (dict(residual=_x(shape=(3, 64))), ValueError), (dict(residual=_x(torch.float64)), TypeError),
+    (dict(residual=_x().transpose(0, 1).contiguous().transpose(0, 1)), ValueError),
+    (dict(out=_x(shape=(15, 64))), ValueError), (dict(out=_x(torch.int32)), TypeError), (dict(h=_x()), ValueError),
+    (dict(residual=_x(), h=_x(F32)), TypeError), (dict(rstd=torch.ones(14)), ValueError),
+    (dict(rstd=torch.ones(15, dtype=torch.float64)), ValueError), (dict(out_dtype=torch.float64), TypeError),
+    (dict(out_dtype=torch.float16), GnError),
+], ids=str)
+def test_forward_binding_refusals(kw, err):
+    with pytest.raises(err):
+        gn.gn_rms_forward(_x(), torch.ones(64), **kw)
+
+
+def test_row_layouts():
+    w = torch.ones(64)
+    for bad in (_x().transpose(1, 2), _x()[..., ::2], _x(shape=(3, 5, 130)).transpose(0, 1)[..., :64],
+                torch.ones(1, dtype=BF).expand(4, 64)):
+        with pytest.raises(ValueError):
+            gn.gn_rms_forward(bad, None)
+    with pytest.raises(ValueError):
+        gn.gn_rms_forward(torch.tensor(1.0), None)
+    with pytest.raises(ValueError):
+        gn.gn_rms_forward(torch.ones(3, 0), None)
+    with pytest.raises(ValueError):
+        gn.gn_rms_forward(_x(), w[:63])
+    with pytest.raises(TypeError):
+        gn.gn_rms_forward(_x(torch.int32), w)
+    for good in (_x(shape=(3, 5, 130))[..., 1:65], _x(shape=(3, 1, 64)).expand(3, 1, 64), _x(shape=(64,))):
+        with pytest.raises(GnError) as e:
+            gn.gn_rms_forward(good, w)
+        assert e.value.status == 8
+
+
+def test_q8_and_backward_binding_refusals():
+    x, w = _x(), torch.ones(64)
+    with pytest.raises(TypeError):
+        gn.gn_rms_forward_q8(x, w, q_dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        gn.gn_rms_forward_q8(x, w, block=32, scale=torch.ones(15))
+    with pytest.raises(TypeError):
+        gn.gn_rms_forward_q8(x, w, out=_x())
+    with pytest.raises(ValueError):
+        gn.gn_q8_dequantize(_x(torch.int8), torch.ones(14))
+    with pytest.raises(TypeError):
+        gn.gn_q8_dequantize(_x(), torch.ones(15))
+    rs = torch.ones(3, 5)
+    for kw, err in ((dict(dh=_x(F32)), TypeError), (dict(dx=_x(F32)), TypeError), (dict(dweight=torch.ones(63)), ValueError),
+                    (dict(dweight=torch.ones(64, dtype=BF)), TypeError),
+                    (dict(workspace=torch.ones(1 << 16, dtype=torch.uint8)[::2]), ValueError),
+                    (dict(workspace=torch.ones(64, dtype=torch.uint8)), GnError)):
+        with pytest.raises(err):
+            gn.gn_rms_backward(x, x, rs, w, **kw)
+    with pytest.raises(ValueError):
+        gn.gn_rms_backward(x[:2], x, rs, w)
+    with pytest.raises(ValueError):
+        gn.gn_rms_backward(x, x, rs[:2], w)
+
+
+def test_gradient_binding_refusals():
+    g = [torch.ones(4, 4), torch.ones(3)]
+    for call, err in ((lambda: gn.gn_grad_norm([]), ValueError), (lambda: gn.gn_grad_norm([g[0][:, ::2]]), ValueError),
+                      (lambda: gn.gn_grad_norm([g[0].to_sparse()]), ValueError),
+                      (lambda: gn.gn_grad_norm([g[0].double()]), TypeError), (lambda: gn.gn_grad_norm(g, 1.0), ValueError),
+                      (lambda: gn.gn_grad_clip(g, 1.0, out=[torch.ones(4, 4)]), ValueError),
+                      (lambda: gn.gn_grad_clip(g[:1], 1.0, out=[torch.ones(4, 4).t()]), ValueError),
+                      (lambda: gn.gn_grad_clip(g[:1], 1.0, out=[torch.ones(16)]), ValueError),
+                      (lambda: gn.gn_grad_clip(g, -1.0), GnError), (lambda: gn.gn_grad_clip([g[0], g[0]], 1.0), GnError),
+                      (lambda: gn.gn_grad_norm(g, norm=torch.ones(2)), ValueError)):
+        with pytest.raises(err):
+            call()
+    assert float(gn.clip_grad_norm_([torch.nn.Parameter(torch.ones(3))], 1.0)) == 0.0   # no gradient anywhere

@@ -18,8 +18,20 @@ STATUS_NAMES = {
     5: "GN_ERR_EPS", 6: "GN_ERR_WORKSPACE", 7: "GN_ERR_ALIGN", 8: "GN_ERR_DEVICE", 9: "GN_ERR_LAUNCH",
     10: "GN_ERR_ACTIVATION", 11: "GN_ERR_LAYOUT", 12: "GN_ERR_SCRATCH",
 }
+# Status codes of include/gn_ops.h.
+OPS_STATUS_NAMES = {32: "GN_ERR_ROWS", 33: "GN_ERR_OVERLAP", 34: "GN_ERR_BLOCK", 35: "GN_ERR_NORM"}
 # Size of the static scratch array that gn_forward_noalloc uses as its workspace.
 GN_NOALLOC_SCRATCH_BYTES = 1 << 20
+
+
+class GnGradTensor(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+    ]
 
 
 class GnPlanInfo(ctypes.Structure):
@@ -99,6 +111,15 @@ def _declare(lib):
         "gn_forward_shard_merge": (I, [P, I64, P, P, I64, I64, I64, I64, F, P, P, P, SZ, P]),
         "gn_backward_shard_sums": (I, [P, I, P, I, P, P, P, P, I, I64, I64, I64, I64, P, P, SZ, P]),
         "gn_backward_shard_merge": (I, [P, I64, P, P, P, P, I64, I64, I64, I64, I64, P, P, P, SZ, P]),
+        "gn_ops_status_string": (ctypes.c_char_p, [I]),
+        "gn_rms_forward": (I, [P, I, I64, P, I, P, I, I64, I64, F, P, I, P, P, P]),
+        "gn_rms_forward_q8": (I, [P, I, I64, P, I, P, I, I64, I64, F, I64, P, I, P, P, P, P]),
+        "gn_q8_dequantize": (I, [P, I, P, I64, I64, I64, P, I, P]),
+        "gn_rms_workspace_bytes": (SZ, [I64, I64]),
+        "gn_rms_backward": (I, [P, I, P, I, I64, P, P, I, P, I64, I64, P, I, P, P, P, SZ, P]),
+        "gn_grad_workspace_bytes": (SZ, [ctypes.POINTER(GnGradTensor), I64]),
+        "gn_grad_norm": (I, [ctypes.POINTER(GnGradTensor), I64, I, P, P, SZ, P]),
+        "gn_grad_clip": (I, [ctypes.POINTER(GnGradTensor), I64, I, F, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

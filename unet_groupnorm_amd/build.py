@@ -3,12 +3,14 @@ libgn_probe.so, the measurement kernels that the benchmark and the tests use bes
 
 libgn.so: the C ABI (csrc/gn_api.cpp), the launch plans (csrc/gn_plan.cpp) and the kernels
 (csrc/gn_kernels.hip for NCDHW, csrc/gn_kernels_cl.hip for channels-last,
-csrc/gn_kernels_shard.hip for spatial shards), compiled with hipcc one source at a time in
-parallel, then linked into ``unet_groupnorm_amd/libgn.so``.
+csrc/gn_kernels_shard.hip for spatial shards), and beside them the row norm and the
+gradient list (csrc/gn_ops_api.cpp, csrc/gn_rms.hip, csrc/gn_grad.hip); compiled with hipcc
+one source at a time in parallel, then linked into ``unet_groupnorm_amd/libgn.so``.
 
-_gnbind (csrc/gn_binding.cpp, a Python extension module linked against libgn.so and torch):
-the compiled marshalling of the per-step calls gn_forward and gn_backward for torch tensors.
-Host code only, compiled with g++ against torch's headers.
+_gnbind (csrc/gn_binding.cpp and csrc/gn_ops_binding.cpp, a Python extension module linked
+against libgn.so and torch): the compiled marshalling of the per-step calls gn_forward and
+gn_backward and of the calls of include/gn_ops.h for torch tensors. Host code only, compiled
+with g++ against torch's headers.
 
 libgn_probe.so (csrc/probe_kernels.hip): streaming read, write and copy kernels that measure
 the device's achievable HBM rates, and an atomic-accumulation reduction kept as the negative
@@ -27,9 +29,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgn.so")
 PROBE_LIB = os.path.join(HERE, "libgn_probe.so")
 OBJDIR = os.path.join(HERE, "_build")
-SOURCES = ["gn_plan.cpp", "gn_api.cpp", "gn_kernels.hip", "gn_kernels_cl.hip", "gn_kernels_shard.hip"]
+SOURCES = ["gn_plan.cpp", "gn_api.cpp", "gn_kernels.hip", "gn_kernels_cl.hip", "gn_kernels_shard.hip",
+           "gn_ops_api.cpp", "gn_rms.hip", "gn_grad.hip"]
 PROBE_SOURCES = ["probe_kernels.hip"]
-BIND_SOURCE = "gn_binding.cpp"
+BIND_SOURCES = ["gn_binding.cpp", "gn_ops_binding.cpp"]
 BIND_NAME = "_gnbind"
 BIND_LIB = os.path.join(HERE, BIND_NAME + sysconfig.get_config_var("EXT_SUFFIX"))
 
@@ -57,21 +60,21 @@ def _run(cmd, verbose):
 
 
 def _bind_commands():
-    """(compile, link) commands of the _gnbind extension module."""
+    """(compile commands, link command) of the _gnbind extension module."""
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
-    obj = os.path.join(OBJDIR, BIND_NAME + ".o")
+    objs = [os.path.join(OBJDIR, f"{BIND_NAME}.{os.path.splitext(s)[0]}.o") for s in BIND_SOURCES]
     inc = [f"-I{p}" for p in include_paths()] + [f"-I{sysconfig.get_paths()['include']}", "-I/opt/rocm/include",
                                                  f"-I{INCLUDE}"]
     defs = ["-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f"-DTORCH_EXTENSION_NAME={BIND_NAME}",
             "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-    compile_cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w"] + defs + inc + \
-        ["-c", os.path.join(CSRC, BIND_SOURCE), "-o", obj]
+    compile_cmds = [["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w"] + defs + inc +
+                    ["-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(BIND_SOURCES, objs)]
     tlib = library_paths()[0]
-    link_cmd = ["g++", "-shared", obj, "-o", BIND_LIB + ".tmp", f"-L{HERE}", "-lgn", "-Wl,-rpath,$ORIGIN",
+    link_cmd = ["g++", "-shared"] + objs + ["-o", BIND_LIB + ".tmp", f"-L{HERE}", "-lgn", "-Wl,-rpath,$ORIGIN",
                 f"-L{tlib}", "-lc10", "-lc10_hip", "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python",
                 f"-Wl,-rpath,{tlib}"]
-    return compile_cmd, link_cmd
+    return compile_cmds, link_cmd
 
 
 def _link(sources, out, extra, verbose, also=()):
@@ -96,7 +99,7 @@ def build(verbose: bool = False, extra=None, out=None) -> str:
         return _link(SOURCES, out, extra, verbose)
     os.makedirs(OBJDIR, exist_ok=True)
     bind_compile, bind_link = _bind_commands()
-    lib = _link(SOURCES, LIB, extra, verbose, also=[bind_compile])
+    lib = _link(SOURCES, LIB, extra, verbose, also=bind_compile)
     _run(bind_link, verbose)
     os.replace(BIND_LIB + ".tmp", BIND_LIB)
     _link(PROBE_SOURCES, PROBE_LIB, extra, verbose)

@@ -221,9 +221,12 @@ py::tuple backward(const at::Tensor& dy, const at::Tensor& x, const c10::optiona
 
 }  // namespace
 
+void bind_ops(pybind11::module_& m);  // gn_ops_binding.cpp
+
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
 {
-    m.doc() = "Compiled marshalling of gn_forward / gn_backward (libgn.so's C ABI) for torch tensors";
+    m.doc() = "Compiled marshalling of libgn.so's C ABI (GroupNorm's per-step calls, the row norm, gradients) for "
+              "torch tensors";
     m.def("forward", &forward, "gn_forward or gn_forward_cl: (y, mean, rstd, status, entry point)", py::arg("x"),
           py::arg("gamma"), py::arg("beta"), py::arg("G"), py::arg("eps"), py::arg("out_code"),
           py::arg("activation"), py::arg("workspace"), py::arg("out"), py::arg("mean"), py::arg("rstd"),
@@ -233,4 +236,5 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
           py::arg("activation"), py::arg("G"), py::arg("need_dx"), py::arg("need_dgamma"), py::arg("need_dbeta"),
           py::arg("workspace"), py::arg("dx"), py::arg("dgamma"), py::arg("dbeta"), py::arg("layout"));
     m.def("abi_version", []() { return gn_abi_version(); });
+    bind_ops(m);
 }

@@ -1,0 +1,130 @@
+// gn_ops.hpp -- kernel arguments and launchers shared by gn_ops_api.cpp and the kernel files
+// of the row norm (gn_rms.hip) and of the gradient list (gn_grad.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gn_ops.h"
+
+namespace gn {
+
+// ------------------------------------------------------------------ row norm
+
+// How a row of H columns is laid over lanes: `lanes` lanes hold one row, each `vecs` vectors
+// of 8 columns (vector v belongs to lane v mod lanes); lanes is a power of two up to 64 with
+// 256 / lanes rows in a workgroup, or a multiple of 64 with one row in a workgroup. A pure
+// function of H, so a row's sums are taken in the same order whatever T is.
+struct RowPlan {
+    int32_t lanes, vecs;
+    int32_t block, rows;  // threads and rows of a workgroup
+    bool exact;           // every lane's vectors are whole and inside the row
+};
+
+// Largest number of vectors a lane holds, and of threads in a workgroup.
+constexpr int kRowMaxVecs = 4;
+constexpr int kRowMaxBlock = 1024;
+static_assert(int64_t(kRowMaxVecs) * kRowMaxBlock * 8 == GN_RMS_MAX_COLUMNS, "widest row");
+
+inline RowPlan row_plan(int64_t H)
+{
+    const int64_t nv = (H + 7) / 8;
+    RowPlan p;
+    if (nv <= 64) {
+        p.lanes = 1;
+        while (p.lanes < nv) p.lanes *= 2;
+        p.vecs = 1;
+        p.block = 256;
+        p.rows = 256 / p.lanes;
+    } else {
+        p.vecs = nv <= 256 ? 1 : nv <= 1024 ? 2 : 4;
+        p.lanes = int32_t(((nv + p.vecs - 1) / p.vecs + 63) / 64 * 64);
+        p.block = p.lanes;
+        p.rows = 1;
+    }
+    p.exact = int64_t(p.lanes) * p.vecs * 8 == H;
+    return p;
+}
+
+// Workgroups of the backward kernel, each taking every P-th group of rows: the partial
+// weight gradients that the second kernel adds.
+constexpr int64_t kRowMaxParts = 1024;
+
+inline int64_t row_parts(int64_t T, const RowPlan& p)
+{
+    const int64_t groups = (T + p.rows - 1) / p.rows;
+    return groups < kRowMaxParts ? groups : kRowMaxParts;
+}
+
+struct RmsArgs {
+    const void* x;
+    const void* res;
+    const void* w;
+    void* h;
+    void* y;       // or q
+    float* rstd;
+    float* scale;
+    int64_t T, H, x_stride;
+    float eps;
+    int32_t w_f32, y_f32;     // weight and y in fp32 (else x's dtype); weight may be null
+    int32_t lanes, rows;
+    int32_t q_dtype, block;   // 8-bit output: format, columns of a scale (0: the row)
+    int64_t scales;           // scales of a row
+};
+
+struct RmsBwdArgs {
+    const void* dy;
+    const void* h;
+    const void* w;
+    const void* dh;
+    const float* rstd;
+    void* dx;
+    void* dres;
+    float* part;   // [parts][H], null: no weight gradient
+    int64_t T, H, h_stride, parts;
+    int32_t w_dtype, x_dtype;  // gn_dtype codes
+    int32_t lanes, rows;
+};
+
+hipError_t launch_rms_fwd(const RmsArgs& a, int x_dtype, int r_dtype, bool q8, const RowPlan& p, hipStream_t st);
+hipError_t launch_rms_bwd(const RmsBwdArgs& a, int dy_dtype, int h_dtype, const RowPlan& p, hipStream_t st);
+// dweight[c] = sum over parts of part[p][c].
+hipError_t launch_rms_dweight(const float* part, int64_t parts, int64_t H, void* dw, int w_dtype, hipStream_t st);
+hipError_t launch_q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, int64_t H, int64_t block,
+                                void* out, int out_dtype, hipStream_t st);
+
+// ------------------------------------------------------------------ gradient list
+
+// Elements of one tile, the unit in which workgroups share out the list; a tile never
+// crosses from one tensor to the next.
+constexpr int64_t kGradTile = 8192;
+// Longest entry of a launch's table (longer tensors take several) and entries of a table,
+// which travels in the kernel's arguments (4 KB at most).
+constexpr int64_t kGradMaxElems = int64_t(1) << 27;
+constexpr int kGradEntries = 160;
+// Workgroups of one launch, hence partial results of a table.
+constexpr int64_t kGradGrid = 2048;
+
+struct GradEntry {
+    const void* data;
+    void* out;
+    uint32_t numel : 28, dtype : 2, out_dtype : 2;
+    uint32_t tile0;  // tiles of the entries before this one
+};
+
+struct GradTable {
+    GradEntry e[kGradEntries];
+    int32_t n;
+    uint32_t tiles;
+};
+static_assert(sizeof(GradTable) + 64 <= 4096, "kernel arguments");
+
+// Partial norms of one table's entries: one fp64 for each of `grid` workgroups.
+hipError_t launch_grad_partials(const GradTable& t, bool inf, double* part, int64_t grid, hipStream_t st);
+// norm[0] from `parts` partials.
+hipError_t launch_grad_norm(const double* part, int64_t parts, bool inf, float* norm, hipStream_t st);
+// out = data * coef for one table; norm[0] is written too where norm is not null.
+hipError_t launch_grad_scale(const GradTable& t, const double* part, int64_t parts, bool inf, float max_norm,
+                             float* norm, int64_t grid, hipStream_t st);
+
+}  // namespace gn
