@@ -148,7 +148,7 @@ int gn_grad_norm(const gn_grad_tensor* tensors, int64_t n, int norm_type, float*
  * infinite one makes coef 0. In place with coef == 1 the tensors are left as they are.
  * Outputs may not overlap one another or another tensor's data (a tensor listed twice).
  */
-int gn_grad_clip(const gn_grad_tensor* tensors, int64_t n, int norm_type, float max_norm, float* norm,
+int gn_grad_clip(const gn_grad_tensor* tensors, int64_t n, int norm_type, double max_norm, float* norm,
                  void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus

@@ -119,7 +119,7 @@ def _declare(lib):
         "gn_rms_backward": (I, [P, I, P, I, I64, P, P, I, P, I64, I64, P, I, P, P, P, SZ, P]),
         "gn_grad_workspace_bytes": (SZ, [ctypes.POINTER(GnGradTensor), I64]),
         "gn_grad_norm": (I, [ctypes.POINTER(GnGradTensor), I64, I, P, P, SZ, P]),
-        "gn_grad_clip": (I, [ctypes.POINTER(GnGradTensor), I64, I, F, P, P, SZ, P]),
+        "gn_grad_clip": (I, [ctypes.POINTER(GnGradTensor), I64, I, ctypes.c_double, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -25,49 +25,155 @@ __device__ __forceinline__ T* out(void* p)
     return static_cast<T*>(p);
 }
 
-template <typename T>
+// One 8-element vector as loaded; NT marks it nontemporal (read or written once).
+template <typename T, bool NT = false>
 __device__ __forceinline__ typename Io<T>::Raw load_any(const T* p)
 {
     typename Io<T>::Raw r;
     if constexpr (sizeof(T) == 4) {
         const f32x4_any* q = reinterpret_cast<const f32x4_any*>(p);
-        r.a = q[0];
-        r.b = q[1];
+        r.a = NT ? __builtin_nontemporal_load(q) : q[0];
+        r.b = NT ? __builtin_nontemporal_load(q + 1) : q[1];
     } else {
-        r.u = *reinterpret_cast<const u32x4_any*>(p);
+        const u32x4_any* q = reinterpret_cast<const u32x4_any*>(p);
+        r.u = NT ? __builtin_nontemporal_load(q) : *q;
     }
     return r;
 }
 
+// The first n (0 to 7) elements of a vector, zeros behind them.
 template <typename T>
+__device__ __forceinline__ typename Io<T>::Raw load_part(const T* p, int n)
+{
+    typename Io<T>::Raw r;
+    if constexpr (sizeof(T) == 4) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.0f;
+        r.a = f32x4{v[0], v[1], v[2], v[3]};
+        r.b = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+        uint32_t v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < n ? uint32_t(q[e]) : 0u;
+        r.u = u32x4{v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16), v[6] | (v[7] << 16)};
+    }
+    return r;
+}
+
+template <typename T, bool NT = false>
 __device__ __forceinline__ void store_any(T* p, const float (&v)[8])
 {
     if constexpr (sizeof(T) == 4) {
         f32x4_any* q = reinterpret_cast<f32x4_any*>(p);
-        q[0] = f32x4{v[0], v[1], v[2], v[3]};
-        q[1] = f32x4{v[4], v[5], v[6], v[7]};
+        const f32x4_any a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        if (NT) {
+            __builtin_nontemporal_store(a, q);
+            __builtin_nontemporal_store(b, q + 1);
+        } else {
+            q[0] = a;
+            q[1] = b;
+        }
     } else {
         alignas(16) T t[8];
         Io<T>::template store8<false>(t, v);
-        *reinterpret_cast<u32x4_any*>(p) = *reinterpret_cast<const u32x4*>(t);
+        const u32x4_any u = *reinterpret_cast<const u32x4*>(t);
+        u32x4_any* q = reinterpret_cast<u32x4_any*>(p);
+        if (NT)
+            __builtin_nontemporal_store(u, q);
+        else
+            *q = u;
     }
-}
-
-// The first n (1 to 7) elements of a vector, zeros behind them.
-template <typename T>
-__device__ __forceinline__ void load_part(const T* p, int n, float (&v)[8])
-{
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? Io<T>::load1(p + e) : 0.0f;
 }
 
 template <typename T>
 __device__ __forceinline__ void store_part(T* p, int n, const float (&v)[8])
 {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < 7; ++e)
         if (e < n) Io<T>::store1(p + e, v[e]);
 }
+
+// W (4 or 8) elements as one lane loads and stores them: fp32 in fours and 16-bit types in
+// eights are 16-byte accesses, 16-bit types in fours 8-byte ones. A wave's accesses cover
+// whole lines in each case; eight fp32 values of one lane would be two accesses that each
+// touch half of every line.
+template <typename T, int W>
+struct Piece {
+    static constexpr int kWords = W * int(sizeof(T)) / 4;
+    static_assert(kWords == 2 || kWords == 4, "8- or 16-byte access");
+    typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+    typedef uint32_t WordsAny __attribute__((ext_vector_type(kWords), aligned(sizeof(T))));
+    Words w;
+
+    template <bool NT>
+    __device__ __forceinline__ void load(const T* p)
+    {
+        const WordsAny* q = reinterpret_cast<const WordsAny*>(p);
+        w = NT ? __builtin_nontemporal_load(q) : *q;
+    }
+    // The first n (below W) elements, zeros behind them.
+    __device__ __forceinline__ void load_part(const T* p, int n)
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) w[e] = e < n ? __float_as_uint(p[e]) : 0u;
+        } else {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+            for (int e = 0; e < W; e += 2)
+                w[e / 2] = (e < n ? uint32_t(q[e]) : 0u) | (e + 1 < n ? uint32_t(q[e + 1]) << 16 : 0u);
+        }
+    }
+    __device__ __forceinline__ void widen(float (&v)[W]) const
+    {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            if constexpr (sizeof(T) == 4)
+                v[e] = __uint_as_float(w[e]);
+            else if constexpr (std::is_same<T, uint16_t>::value)
+                v[e] = e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+            else
+                v[e] = e & 1 ? Io<_Float16>::hi(w[e / 2]) : Io<_Float16>::lo(w[e / 2]);
+        }
+    }
+    __device__ __forceinline__ void narrow(const float (&v)[W])
+    {
+#pragma unroll
+        for (int e = 0; e < kWords; ++e) {
+            if constexpr (sizeof(T) == 4)
+                w[e] = __float_as_uint(v[e]);
+            else if constexpr (std::is_same<T, uint16_t>::value)
+                w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            else
+                w[e] = Io<_Float16>::pack(v[2 * e], v[2 * e + 1]);
+        }
+    }
+    template <bool NT>
+    __device__ __forceinline__ void store(T* p) const
+    {
+        WordsAny* q = reinterpret_cast<WordsAny*>(p);
+        const WordsAny t = w;
+        if (NT)
+            __builtin_nontemporal_store(t, q);
+        else
+            *q = t;
+    }
+    __device__ __forceinline__ void store_part(T* p, int n) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (e < n) p[e] = __uint_as_float(w[e]);
+        } else {
+            uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+                if (e < n) q[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
+        }
+    }
+};
 
 }  // namespace
 

@@ -14,11 +14,17 @@ namespace gn {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kTileVecs = int(kGradTile / (8 * kBlock));  // 8-element vectors of a lane in a tile
+// A lane's vectors of a step are in flight together.
+constexpr int kStepTiles = int(kGradStep);
+// Loads are nontemporal, in both passes: 613 -> 566 us for 420M bf16 gradients clipped into
+// fp32, 55 -> 51 us for 23M fp32 ones.
+constexpr bool kNt = true;
+// Registers are held to what lets every workgroup of a grid of 8 for each CU be resident.
+constexpr int kWavesPerSimd = 8;
+static_assert(kGradTile == kBlock * 8, "a vector for each lane in a tile");
 
-// A lane's running result: the sum of squares in fp64 (the square of any fp32 value is
-// exact there, and none overflows or vanishes), or the bits of the largest magnitude (which
-// order a NaN above everything).
+// A lane's running result: the sum of squares in fp64, or the bits of the largest magnitude
+// (which order a NaN above everything).
 struct Acc {
     double s = 0.0;
     uint32_t m = 0;
@@ -30,6 +36,25 @@ struct Acc {
             m = b > m ? b : m;
         } else {
             s = fma(double(v), double(v), s);
+        }
+    }
+    // The squares of a piece are added in fp32 and their sum in fp64: an eighth to a quarter of
+    // the fp64 work. Where that sum leaves the range in which fp32 keeps all of it (a square
+    // that overflows, one that is lost below 2^-126 next to a sum under 2^-90), the piece is
+    // taken element by element in fp64, in which the square of any fp32 value is exact.
+    template <bool INF, int W>
+    __device__ __forceinline__ void take(const float (&v)[W])
+    {
+        if constexpr (INF) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) take<INF>(v[e]);
+        } else {
+            const float q = tree_sumsq(v);
+            if (q >= 0x1p-90f && q < __builtin_inff())
+                s = s + double(q);
+            else
+#pragma unroll
+                for (int e = 0; e < W; ++e) take<INF>(v[e]);
         }
     }
 };
@@ -55,82 +80,124 @@ __device__ __forceinline__ double block_join(double v, double* s)
     return r;
 }
 
-// The tiles of workgroup b: [b * tiles / grid, (b + 1) * tiles / grid).
-__device__ __forceinline__ uint32_t first_tile(uint32_t tiles, uint32_t b, uint32_t grid)
+// The launch's table in LDS. A search through it where it arrives, in the kernel's
+// arguments, is a chain of dependent reads of memory that no cache of the chip holds yet:
+// here every entry is read at once.
+struct Shared {
+    GradEntry e[kGradEntries];
+    double part[kBlock / 64];
+};
+
+__device__ __forceinline__ void stage(const GradTable& t, Shared& s)
 {
-    return uint32_t(uint64_t(tiles) * b / grid);
+    static_assert(kGradEntries <= kBlock, "an entry for each lane");
+    if (int(threadIdx.x) < t.n) s.e[threadIdx.x] = t.e[threadIdx.x];
 }
 
-// The entry that holds tile k.
-__device__ __forceinline__ int entry_of(const GradTable& t, uint32_t k)
+// An entry with its words in scalar registers (all lanes read the same one).
+__device__ __forceinline__ GradEntry uniform_entry(const GradEntry& e)
 {
-    int lo = 0, hi = t.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t.e[mid].tile0 <= k) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+    struct Words {
+        uint32_t w[sizeof(GradEntry) / 4];
+    };
+    Words x = __builtin_bit_cast(Words, e);
+#pragma unroll
+    for (uint32_t& w : x.w) w = uint32_t(__builtin_amdgcn_readfirstlane(int(w)));
+    return __builtin_bit_cast(GradEntry, x);
 }
 
-// Calls f(entry, first element, elements) for each tile of this workgroup.
+// Calls f(entry, first element, elements) over this workgroup's tiles: of the list's steps of
+// kStepTiles tiles it takes steps blockIdx.x, blockIdx.x + gridDim.x, ..., so that the whole
+// launch moves over the list together, each step split where an entry ends in it. Every lane
+// takes part; the table is staged and the workgroup synchronized before.
 template <typename F>
-__device__ __forceinline__ void for_tiles(const GradTable& t, F&& f)
+__device__ __forceinline__ void for_tiles(const Shared& s, int n, uint32_t tiles, F&& f)
 {
-    uint32_t k = first_tile(t.tiles, blockIdx.x, gridDim.x);
-    const uint32_t end = first_tile(t.tiles, blockIdx.x + 1, gridDim.x);
-    if (k >= end) return;
-    int i = entry_of(t, k);
-    for (; k < end; ++k) {
-        while (i + 1 < t.n && t.e[i + 1].tile0 <= k) ++i;
-        const uint32_t at = (k - t.e[i].tile0) * uint32_t(kGradTile);
-        const uint32_t left = t.e[i].numel - at;
-        f(t.e[i], at, left < kGradTile ? int(left) : int(kGradTile));
+    const auto tile0 = [&](int i) {
+        return i < n ? uint32_t(__builtin_amdgcn_readfirstlane(int(s.e[i].tile0))) : tiles;
+    };
+    const uint32_t steps = (tiles + kStepTiles - 1) / kStepTiles;
+    int i = 0;
+    for (uint32_t step = blockIdx.x; step < steps; step += gridDim.x) {
+        uint32_t k = step * kStepTiles;
+        const uint32_t end = k + kStepTiles < tiles ? k + kStepTiles : tiles;
+        int hi = n - 1;  // the entry of tile k, behind the last one taken
+        while (i < hi) {
+            const int mid = (i + hi + 1) >> 1;
+            if (tile0(mid) <= k) i = mid;
+            else hi = mid - 1;
+        }
+        for (int j = i; k < end; ++j) {
+            const GradEntry e = uniform_entry(s.e[j]);
+            const uint32_t last = tile0(j + 1), t1 = end < last ? end : last;
+            const uint32_t at = (k - e.tile0) * uint32_t(kGradTile), left = e.numel - at;
+            const uint32_t most = (t1 - k) * uint32_t(kGradTile);
+            k = t1;
+            f(e, at, int(left < most ? left : most));
+        }
     }
 }
 
-template <typename T, bool INF>
-__device__ __forceinline__ void tile_norm(const T* p, int n, Acc& acc)
+// Calls f(first element, values) for each of the lane's whole pieces of W elements in a step
+// of n, whose loads are all issued first, and g(element, value) for an element behind them.
+template <typename T, int W, typename F, typename G>
+__device__ __forceinline__ void for_pieces(const T* p, int n, F&& f, G&& g)
 {
+    constexpr int kPieces = int(kStepTiles * kGradTile) / (W * kBlock);
     const int tid = threadIdx.x;
-    if (n == kGradTile) {
-        typename Io<T>::Raw raw[kTileVecs];
+    Piece<T, W> raw[kPieces];
+    if (n == kStepTiles * kGradTile) {
 #pragma unroll
-        for (int u = 0; u < kTileVecs; ++u) raw[u] = load_any(p + (u * kBlock + tid) * 8);
+        for (int u = 0; u < kPieces; ++u) raw[u].template load<kNt>(p + (u * kBlock + tid) * W);
 #pragma unroll
-        for (int u = 0; u < kTileVecs; ++u) {
-            float v[8];
-            Io<T>::widen(raw[u], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc.take<INF>(v[e]);
+        for (int u = 0; u < kPieces; ++u) {
+            float v[W];
+            raw[u].widen(v);
+            f((u * kBlock + tid) * W, v);
         }
         return;
     }
-    const int full = n >> 3;
-    for (int i = tid; i < full; i += kBlock) {
-        float v[8];
-        Io<T>::widen(load_any(p + i * 8), v);
+    const int full = n / W, behind = n % W;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc.take<INF>(v[e]);
-    }
-    if (tid < (n & 7)) acc.take<INF>(Io<T>::load1(p + full * 8 + tid));
+    for (int u = 0; u < kPieces; ++u)
+        if (u * kBlock + tid < full) raw[u].template load<kNt>(p + (u * kBlock + tid) * W);
+    float last = 0.0f;
+    if (tid < behind) last = Io<T>::load1(p + full * W + tid);
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u)
+        if (u * kBlock + tid < full) {
+            float v[W];
+            raw[u].widen(v);
+            f((u * kBlock + tid) * W, v);
+        }
+    if (tid < behind) g(full * W + tid, last);
+}
+
+template <typename T, bool INF>
+__device__ __forceinline__ void step_norm(const T* p, int n, Acc& acc)
+{
+    constexpr int W = sizeof(T) == 4 ? 4 : 8;
+    for_pieces<T, W>(
+        p, n, [&](int, const float(&v)[W]) { acc.take<INF, W>(v); }, [&](int, float v) { acc.take<INF>(v); });
 }
 
 template <bool INF>
-__global__ void __launch_bounds__(kBlock)
+__global__ void __launch_bounds__(kBlock, kWavesPerSimd)
 grad_partials_kernel(GradTable t, double* part)
 {
-    __shared__ double s[kBlock / 64];
+    __shared__ Shared s;
+    stage(t, s);
+    __syncthreads();
     Acc acc;
-    for_tiles(t, [&](const GradEntry& e, uint32_t at, int n) {
+    for_tiles(s, t.n, t.tiles, [&](const GradEntry& e, uint32_t at, int n) {
         if (e.dtype == GN_BF16)
-            tile_norm<uint16_t, INF>(in<uint16_t>(e.data) + at, n, acc);
+            step_norm<uint16_t, INF>(in<uint16_t>(e.data) + at, n, acc);
         else if (e.dtype == GN_F16)
-            tile_norm<_Float16, INF>(in<_Float16>(e.data) + at, n, acc);
+            step_norm<_Float16, INF>(in<_Float16>(e.data) + at, n, acc);
         else
-            tile_norm<float, INF>(in<float>(e.data) + at, n, acc);
+            step_norm<float, INF>(in<float>(e.data) + at, n, acc);
     });
-    const double r = block_join<INF>(INF ? double(__uint_as_float(acc.m)) : acc.s, s);
+    const double r = block_join<INF>(INF ? double(__uint_as_float(acc.m)) : acc.s, s.part);
     if (threadIdx.x == 0) part[blockIdx.x] = r;
 }
 
@@ -139,73 +206,79 @@ template <bool INF>
 __device__ __forceinline__ double norm_of(const double* part, int64_t parts, double* s)
 {
     double v = 0.0;
+#pragma unroll 8
     for (int64_t p = threadIdx.x; p < parts; p += kBlock) v = join<INF>(v, part[p]);
     v = block_join<INF>(v, s);
     return INF ? v : sqrt(v);
 }
 
+template <bool NT, typename T, typename O>
+__device__ __forceinline__ void step_scale(const T* p, O* o, int n, float coef)
+{
+    constexpr int W = sizeof(O) == 4 ? 4 : 8;
+    for_pieces<T, W>(
+        p, n,
+        [&](int i, const float(&v)[W]) {
+            float w[W];
+#pragma unroll
+            for (int e = 0; e < W; ++e) w[e] = v[e] * coef;
+            Piece<O, W> q;
+            q.narrow(w);
+            q.template store<NT>(o + i);
+        },
+        [&](int i, float v) { Io<O>::store1(o + i, v * coef); });
+}
+
+// coef from the norm; a NaN stays.
+__device__ __forceinline__ float coef_of(double norm, double max_norm)
+{
+    const double c = max_norm / (norm + 1e-6);
+    return c >= 1.0 ? 1.0f : float(c);
+}
+
+// norm[0], and the factor where coef is not null.
 template <bool INF>
 __global__ void __launch_bounds__(kBlock)
-grad_norm_kernel(const double* part, int64_t parts, float* norm)
+grad_norm_kernel(const double* part, int64_t parts, double max_norm, float* norm, float* coef)
 {
     __shared__ double s[kBlock / 64];
     const double v = norm_of<INF>(part, parts, s);
-    if (threadIdx.x == 0) norm[0] = float(v);
+    if (threadIdx.x != 0) return;
+    norm[0] = float(v);
+    if (coef) coef[0] = coef_of(v, max_norm);
 }
 
-template <typename T, typename O>
-__device__ __forceinline__ void tile_scale(const T* p, O* o, int n, float coef)
+// FOLD: every workgroup takes the norm from the partials itself (norm is then written too,
+// where it is not null); otherwise grad_norm_kernel has left the factor in ready[0]. That
+// form, for long lists, stores nontemporally (857 -> 838 us for 420M fp32 gradients); outputs
+// that the last-level cache holds are stored plainly (51 -> 49 us for 23M).
+template <bool INF, bool FOLD>
+__global__ void __launch_bounds__(kBlock, kWavesPerSimd)
+grad_scale_kernel(GradTable t, const double* part, int64_t parts, double max_norm, float* norm, const float* ready)
 {
-    const int tid = threadIdx.x;
-    if (n == kGradTile) {
-        typename Io<T>::Raw raw[kTileVecs];
-#pragma unroll
-        for (int u = 0; u < kTileVecs; ++u) raw[u] = load_any(p + (u * kBlock + tid) * 8);
-#pragma unroll
-        for (int u = 0; u < kTileVecs; ++u) {
-            float v[8];
-            Io<T>::widen(raw[u], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * coef;
-            store_any(o + (u * kBlock + tid) * 8, v);
-        }
-        return;
+    __shared__ Shared s;
+    stage(t, s);
+    float coef;
+    if constexpr (FOLD) {
+        const double v = norm_of<INF>(part, parts, s.part);  // synchronizes
+        if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = float(v);
+        coef = coef_of(v, max_norm);
+    } else {
+        coef = ready[0];
+        __syncthreads();
     }
-    const int full = n >> 3;
-    for (int i = tid; i < full; i += kBlock) {
-        float v[8];
-        Io<T>::widen(load_any(p + i * 8), v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * coef;
-        store_any(o + i * 8, v);
-    }
-    if (tid < (n & 7)) {
-        const int i = full * 8 + tid;
-        Io<O>::store1(o + i, Io<T>::load1(p + i) * coef);
-    }
-}
-
-template <bool INF>
-__global__ void __launch_bounds__(kBlock)
-grad_scale_kernel(GradTable t, const double* part, int64_t parts, float max_norm, float* norm)
-{
-    __shared__ double s[kBlock / 64];
-    const double v = norm_of<INF>(part, parts, s);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = float(v);
-    const double c = double(max_norm) / (v + 1e-6);
-    const float coef = c >= 1.0 ? 1.0f : float(c);  // a NaN stays
-    for_tiles(t, [&](const GradEntry& e, uint32_t at, int n) {
+    for_tiles(s, t.n, t.tiles, [&](const GradEntry& e, uint32_t at, int n) {
         if (coef == 1.0f && e.data == e.out) return;
         if (e.dtype == GN_BF16) {
             const uint16_t* p = in<uint16_t>(e.data) + at;
-            if (e.out_dtype == GN_F32) tile_scale(p, out<float>(e.out) + at, n, coef);
-            else tile_scale(p, out<uint16_t>(e.out) + at, n, coef);
+            if (e.out_dtype == GN_F32) step_scale<!FOLD>(p, out<float>(e.out) + at, n, coef);
+            else step_scale<!FOLD>(p, out<uint16_t>(e.out) + at, n, coef);
         } else if (e.dtype == GN_F16) {
             const _Float16* p = in<_Float16>(e.data) + at;
-            if (e.out_dtype == GN_F32) tile_scale(p, out<float>(e.out) + at, n, coef);
-            else tile_scale(p, out<_Float16>(e.out) + at, n, coef);
+            if (e.out_dtype == GN_F32) step_scale<!FOLD>(p, out<float>(e.out) + at, n, coef);
+            else step_scale<!FOLD>(p, out<_Float16>(e.out) + at, n, coef);
         } else {
-            tile_scale(in<float>(e.data) + at, out<float>(e.out) + at, n, coef);
+            step_scale<!FOLD>(in<float>(e.data) + at, out<float>(e.out) + at, n, coef);
         }
     });
 }
@@ -218,17 +291,20 @@ hipError_t launch_grad_partials(const GradTable& t, bool inf, double* part, int6
                : launch(grad_partials_kernel<false>, dim3(unsigned(grid)), dim3(kBlock), st, t, part);
 }
 
-hipError_t launch_grad_norm(const double* part, int64_t parts, bool inf, float* norm, hipStream_t st)
+hipError_t launch_grad_norm(const double* part, int64_t parts, bool inf, double max_norm, float* norm, float* coef,
+                            hipStream_t st)
 {
-    return inf ? launch(grad_norm_kernel<true>, dim3(1), dim3(kBlock), st, part, parts, norm)
-               : launch(grad_norm_kernel<false>, dim3(1), dim3(kBlock), st, part, parts, norm);
+    return inf ? launch(grad_norm_kernel<true>, dim3(1), dim3(kBlock), st, part, parts, max_norm, norm, coef)
+               : launch(grad_norm_kernel<false>, dim3(1), dim3(kBlock), st, part, parts, max_norm, norm, coef);
 }
 
-hipError_t launch_grad_scale(const GradTable& t, const double* part, int64_t parts, bool inf, float max_norm,
-                             float* norm, int64_t grid, hipStream_t st)
+hipError_t launch_grad_scale(const GradTable& t, const double* part, int64_t parts, bool inf, double max_norm,
+                             float* norm, const float* ready, int64_t grid, hipStream_t st)
 {
-    return inf ? launch(grad_scale_kernel<true>, dim3(unsigned(grid)), dim3(kBlock), st, t, part, parts, max_norm, norm)
-               : launch(grad_scale_kernel<false>, dim3(unsigned(grid)), dim3(kBlock), st, t, part, parts, max_norm, norm);
+    const dim3 g = dim3(unsigned(grid)), b = dim3(kBlock);
+    if (ready) return launch(grad_scale_kernel<false, false>, g, b, st, t, part, parts, max_norm, norm, ready);
+    return inf ? launch(grad_scale_kernel<true, true>, g, b, st, t, part, parts, max_norm, norm, ready)
+               : launch(grad_scale_kernel<false, true>, g, b, st, t, part, parts, max_norm, norm, ready);
 }
 
 }  // namespace gn

@@ -46,15 +46,33 @@ inline RowPlan row_plan(int64_t H)
     return p;
 }
 
-// Workgroups of the backward kernel, each taking every P-th group of rows: the partial
-// weight gradients that the second kernel adds.
-constexpr int64_t kRowMaxParts = 1024;
+// The backward's plan: the same lanes for a row, as many rows at once as a workgroup of 512
+// threads holds (fewer where T rows would not fill the chip with such workgroups), and the
+// workgroups, each taking every parts-th group of rows and leaving one partial weight
+// gradient.
+struct BwdPlan : RowPlan {
+    int64_t parts;
+};
 
-inline int64_t row_parts(int64_t T, const RowPlan& p)
+constexpr int kBwdBlock = 512;
+constexpr int64_t kBwdParts = 256;
+
+inline BwdPlan bwd_plan(int64_t T, int64_t H)
 {
+    BwdPlan p;
+    static_cast<RowPlan&>(p) = row_plan(H);
+    const int32_t least = p.lanes < 64 ? 64 / p.lanes : 1;  // rows of a whole wave
+    int64_t rows = kBwdBlock / p.lanes;
+    while (rows > least && (T + rows - 1) / rows < kBwdParts) rows /= 2;
+    p.rows = int32_t(rows < least ? least : rows);
+    p.block = p.rows * p.lanes;
     const int64_t groups = (T + p.rows - 1) / p.rows;
-    return groups < kRowMaxParts ? groups : kRowMaxParts;
+    p.parts = groups < kBwdParts ? groups : kBwdParts;
+    return p;
 }
+
+// Calls that move more than this many bytes take their rows with nontemporal accesses.
+constexpr int64_t kRowStreamBytes = int64_t(160) << 20;
 
 struct RmsArgs {
     const void* x;
@@ -70,6 +88,7 @@ struct RmsArgs {
     int32_t lanes, rows;
     int32_t q_dtype, block;   // 8-bit output: format, columns of a scale (0: the row)
     int64_t scales;           // scales of a row
+    bool nt;                  // nontemporal loads and stores of the rows
 };
 
 struct RmsBwdArgs {
@@ -84,10 +103,11 @@ struct RmsBwdArgs {
     int64_t T, H, h_stride, parts;
     int32_t w_dtype, x_dtype;  // gn_dtype codes
     int32_t lanes, rows;
+    bool nt;                   // nontemporal loads and stores of the rows
 };
 
 hipError_t launch_rms_fwd(const RmsArgs& a, int x_dtype, int r_dtype, bool q8, const RowPlan& p, hipStream_t st);
-hipError_t launch_rms_bwd(const RmsBwdArgs& a, int dy_dtype, int h_dtype, const RowPlan& p, hipStream_t st);
+hipError_t launch_rms_bwd(const RmsBwdArgs& a, int dy_dtype, int h_dtype, const BwdPlan& p, hipStream_t st);
 // dweight[c] = sum over parts of part[p][c].
 hipError_t launch_rms_dweight(const float* part, int64_t parts, int64_t H, void* dw, int w_dtype, hipStream_t st);
 hipError_t launch_q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, int64_t H, int64_t block,
@@ -97,13 +117,20 @@ hipError_t launch_q8_dequantize(const void* q, int q_dtype, const float* scale, 
 
 // Elements of one tile, the unit in which workgroups share out the list; a tile never
 // crosses from one tensor to the next.
-constexpr int64_t kGradTile = 8192;
+constexpr int64_t kGradTile = 2048;
+// Tiles that a workgroup takes at once.
+constexpr int64_t kGradStep = 4;
 // Longest entry of a launch's table (longer tensors take several) and entries of a table,
 // which travels in the kernel's arguments (4 KB at most).
 constexpr int64_t kGradMaxElems = int64_t(1) << 27;
 constexpr int kGradEntries = 160;
-// Workgroups of one launch, hence partial results of a table.
+// Workgroups of the launches over a list together, hence its partial results (and one more
+// for each further table at most).
 constexpr int64_t kGradGrid = 2048;
+// Lists of more tiles than this are scaled by one workgroup for each step, after a kernel
+// that takes the norm and the factor from the partials; in shorter ones each of up to
+// kGradGrid workgroups does that itself.
+constexpr int64_t kGradFoldTiles = 32768;
 
 struct GradEntry {
     const void* data;
@@ -121,10 +148,12 @@ static_assert(sizeof(GradTable) + 64 <= 4096, "kernel arguments");
 
 // Partial norms of one table's entries: one fp64 for each of `grid` workgroups.
 hipError_t launch_grad_partials(const GradTable& t, bool inf, double* part, int64_t grid, hipStream_t st);
-// norm[0] from `parts` partials.
-hipError_t launch_grad_norm(const double* part, int64_t parts, bool inf, float* norm, hipStream_t st);
-// out = data * coef for one table; norm[0] is written too where norm is not null.
-hipError_t launch_grad_scale(const GradTable& t, const double* part, int64_t parts, bool inf, float max_norm,
-                             float* norm, int64_t grid, hipStream_t st);
+// norm[0] from `parts` partials, and the factor where coef is not null.
+hipError_t launch_grad_norm(const double* part, int64_t parts, bool inf, double max_norm, float* norm, float* coef,
+                            hipStream_t st);
+// out = data * coef for one table. ready null: each workgroup takes the norm from the partials
+// and norm[0] is written too where norm is not null; else coef is ready[0].
+hipError_t launch_grad_scale(const GradTable& t, const double* part, int64_t parts, bool inf, double max_norm,
+                             float* norm, const float* ready, int64_t grid, hipStream_t st);
 
 }  // namespace gn

@@ -13,6 +13,7 @@
 
 #include "gn_ops.h"
 #include "gn_ops.hpp"
+#include "gn_ops_internal.hpp"
 
 namespace {
 
@@ -157,6 +158,7 @@ int forward(const void* x, int x_dtype, int64_t x_stride, const void* res, int r
     a.q_dtype = q_dtype;
     a.block = int32_t(block);
     a.scales = scales;
+    a.nt = T * H * (size_of(x_dtype) + ys + (res ? 2 * size_of(r_dtype) : 0)) > gn::kRowStreamBytes;
     for (int64_t t = 0; t < T; t += kMaxGroups * p.rows) {
         a.T = std::min(T - t, kMaxGroups * p.rows);
         a.x = at(x, t * x_stride * size_of(x_dtype));
@@ -190,31 +192,32 @@ int tensors_check(const gn_grad_tensor* t, int64_t n, bool clip)
 }
 
 // Whether every output is apart from every other output and from every other tensor's data.
-// Spans in the order given are often ascending already (a model's gradients in one buffer).
+// Both lists are often ascending already (a model's gradients in one buffer).
 bool outputs_apart(const gn_grad_tensor* t, int64_t n)
-{
-    struct Piece {
-        uintptr_t b, e;
-        bool out;
-    };
-    std::vector<Piece> s;
-    s.reserve(size_t(2 * n));
+try {
+    std::vector<Span> outs, ins;
+    outs.reserve(size_t(n));
+    ins.reserve(size_t(n));
     for (int64_t i = 0; i < n; ++i) {
         if (t[i].numel == 0) continue;
         const Span d(t[i].data, t[i].numel * size_of(t[i].dtype)), o(t[i].out, t[i].numel * size_of(t[i].out_dtype));
-        s.push_back(Piece{o.b, o.e, true});
-        if (d.is(o) && t[i].dtype == t[i].out_dtype) continue;
-        s.push_back(Piece{d.b, d.e, false});
+        outs.push_back(o);
+        if (!(d.is(o) && t[i].dtype == t[i].out_dtype)) ins.push_back(d);
     }
-    const auto before = [](const Piece& a, const Piece& b) { return a.b < b.b; };
-    if (!std::is_sorted(s.begin(), s.end(), before)) std::sort(s.begin(), s.end(), before);
-    uintptr_t out_end = 0, any_end = 0;
-    for (const Piece& p : s) {
-        if (p.b < out_end || (p.out && p.b < any_end)) return false;
-        if (p.out) out_end = std::max(out_end, p.e);
-        any_end = std::max(any_end, p.e);
+    const auto before = [](const Span& a, const Span& b) { return a.b < b.b; };
+    for (std::vector<Span>* v : {&outs, &ins})
+        if (!std::is_sorted(v->begin(), v->end(), before)) std::sort(v->begin(), v->end(), before);
+    for (size_t i = 1; i < outs.size(); ++i)
+        if (outs[i].b < outs[i - 1].e) return false;
+    // Inputs may overlap one another: walk the outputs past those that end before each input.
+    size_t k = 0;
+    for (const Span& d : ins) {
+        while (k < outs.size() && outs[k].e <= d.b) ++k;
+        if (k < outs.size() && outs[k].b < d.e) return false;
     }
     return true;
+} catch (const std::bad_alloc&) {  // nothing is thrown across the ABI: out of host memory, the call is refused
+    return false;
 }
 
 // The list cut into tables: entries of at most kGradMaxElems elements, empty tensors left
@@ -250,30 +253,50 @@ int for_tables(const gn_grad_tensor* t, int64_t n, F&& f)
     return tab.n || !any ? flush() : GN_OK;
 }
 
-int64_t grid_of_table(const gn::GradTable& t) { return std::max<int64_t>(1, std::min<int64_t>(t.tiles, gn::kGradGrid)); }
+// Tiles of the whole list.
+int64_t tiles_of(const gn_grad_tensor* t, int64_t n)
+{
+    int64_t tiles = 0;
+    for (int64_t i = 0; i < n; ++i)  // an entry's last tile may be short, whole ones divide kGradMaxElems
+        tiles += (t[i].numel + gn::kGradTile - 1) / gn::kGradTile;
+    return tiles;
+}
+static_assert(gn::kGradMaxElems % gn::kGradTile == 0, "tiles of a long tensor");
 
-// Partials of the whole list (a count from the sizes alone).
+// A table's workgroups: its share of `grid` by tiles, with no more than a step's work for
+// each, and one at least.
+int64_t grid_of_table(const gn::GradTable& t, int64_t tiles, int64_t grid)
+{
+    const int64_t steps = (int64_t(t.tiles) + gn::kGradStep - 1) / gn::kGradStep;
+    return std::max<int64_t>(1, std::min(steps, int64_t(t.tiles) * grid / std::max<int64_t>(tiles, 1)));
+}
+
+// Partials of the whole list (a count from the sizes alone); the workspace holds one word
+// more, the factor.
 int64_t partials_of(const gn_grad_tensor* t, int64_t n)
 {
+    const int64_t tiles = tiles_of(t, n);
     int64_t parts = 0;
     (void)for_tables(t, n, [&](const gn::GradTable& tab) {
-        parts += grid_of_table(tab);
+        parts += grid_of_table(tab, tiles, gn::kGradGrid);
         return GN_OK;
     });
     return parts;
 }
 
-int grads(const gn_grad_tensor* t, int64_t n, int norm_type, bool clip, float max_norm, float* norm, void* ws,
-          size_t ws_bytes, void* stream)
+}  // namespace
+
+int gn::grads(const gn_grad_tensor* t, int64_t n, int norm_type, bool clip, double max_norm, float* norm, void* ws,
+              size_t ws_bytes, void* stream, bool devices_known)
 {
     int rc = tensors_check(t, n, clip);
     if (rc) return rc;
-    if ((norm_type != GN_NORM_2 && norm_type != GN_NORM_INF) || (clip && !(max_norm >= 0.0f))) return GN_ERR_NORM;
+    if ((norm_type != GN_NORM_2 && norm_type != GN_NORM_INF) || (clip && !(max_norm >= 0.0))) return GN_ERR_NORM;
     if (!norm || !ws) return GN_ERR_NULL;
     if (!aligned(norm, 4) || !aligned(ws, 16)) return GN_ERR_ALIGN;
-    const int64_t parts = partials_of(t, n);
-    if (ws_bytes < size_t(parts) * sizeof(double)) return GN_ERR_WORKSPACE;
-    const Span sn(norm, 4), sws(ws, parts * int64_t(sizeof(double)));
+    const int64_t parts = partials_of(t, n), tiles = tiles_of(t, n);
+    if (ws_bytes < size_t(parts + 1) * sizeof(double)) return GN_ERR_WORKSPACE;
+    const Span sn(norm, 4), sws(ws, (parts + 1) * int64_t(sizeof(double)));
     if (sn.meets(sws) || (clip && !outputs_apart(t, n))) return GN_ERR_OVERLAP;
     for (int64_t i = 0; i < n; ++i) {
         const Span d(t[i].data, t[i].numel * size_of(t[i].dtype)),
@@ -282,7 +305,7 @@ int grads(const gn_grad_tensor* t, int64_t n, int norm_type, bool clip, float ma
     }
     OnDeviceOf dev;
     if ((rc = dev.enter(norm, stream)) || (rc = dev.holds({ws}))) return rc;
-    for (int64_t i = 0; i < n; ++i)
+    for (int64_t i = 0; i < n && !devices_known; ++i)
         if (t[i].numel && ((rc = dev.holds({t[i].data})) || (clip && t[i].out != t[i].data && (rc = dev.holds({t[i].out})))))
             return rc;
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -290,22 +313,26 @@ int grads(const gn_grad_tensor* t, int64_t n, int norm_type, bool clip, float ma
     double* part = static_cast<double*>(ws);
     int64_t done = 0;
     rc = for_tables(t, n, [&](const gn::GradTable& tab) {
-        const int64_t g = grid_of_table(tab);
+        const int64_t g = grid_of_table(tab, tiles, gn::kGradGrid);
         const int s = launch_status(gn::launch_grad_partials(tab, inf, part + done, g, st));
         done += g;
         return s;
     });
     if (rc) return rc;
-    if (!clip) return launch_status(gn::launch_grad_norm(part, parts, inf, norm, st));
-    float* out = norm;
+    const bool fold = clip && tiles <= gn::kGradFoldTiles;
+    float* coef = reinterpret_cast<float*>(part + parts);
+    if (!fold) {
+        rc = launch_status(gn::launch_grad_norm(part, parts, inf, max_norm, norm, clip ? coef : nullptr, st));
+        if (rc || !clip) return rc;
+    }
+    float* out = fold ? norm : nullptr;
     return for_tables(t, n, [&](const gn::GradTable& tab) {
-        const int s = launch_status(gn::launch_grad_scale(tab, part, parts, inf, max_norm, out, grid_of_table(tab), st));
+        const int64_t g = grid_of_table(tab, tiles, fold ? gn::kGradGrid : kMaxGroups);
+        const int s = launch_status(gn::launch_grad_scale(tab, part, parts, inf, max_norm, out, fold ? nullptr : coef, g, st));
         out = nullptr;  // written once
         return s;
     });
 }
-
-}  // namespace
 
 extern "C" {
 
@@ -362,8 +389,7 @@ int gn_q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, 
 size_t gn_rms_workspace_bytes(int64_t T, int64_t H)
 {
     if (rows_check(T, H, H)) return 0;
-    const int64_t parts = gn::row_parts(T, gn::row_plan(H));
-    return size_t(std::max<int64_t>(parts, 1)) * size_t(H) * sizeof(float);
+    return size_t(std::max<int64_t>(gn::bwd_plan(T, H).parts, 1)) * size_t(H) * sizeof(float);
 }
 
 int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, int64_t h_stride,
@@ -394,8 +420,8 @@ int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, in
         !aligned(weight, size_of(w_dtype)) || !aligned(dh, size_of(h_dtype)) || !aligned(dx, size_of(x_dtype)) ||
         !aligned(dres, size_of(h_dtype)))
         return GN_ERR_ALIGN;
-    const gn::RowPlan p = gn::row_plan(H);
-    const int64_t parts = gn::row_parts(T, p);
+    const gn::BwdPlan p = gn::bwd_plan(T, H);
+    const int64_t parts = p.parts;
     const Span sy(dy, T * H * size_of(dy_dtype)), sh(h, rows_bytes(T, H, h_stride, h_dtype)), ss(rstd, T * 4),
         sw(weight, H * size_of(w_dtype)), sd(dh, T * H * size_of(h_dtype)), ox(dx, T * H * size_of(x_dtype)),
         orr(dres, T * H * size_of(h_dtype)), ow(dweight, H * size_of(w_dtype)),
@@ -430,31 +456,27 @@ int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, in
     a.x_dtype = x_dtype;
     a.lanes = p.lanes;
     a.rows = p.rows;
+    a.nt = T * H * (size_of(dy_dtype) + size_of(h_dtype) * (dh ? 2 : 1) + (dx ? size_of(x_dtype) : 0) +
+                    (dres ? size_of(h_dtype) : 0)) > gn::kRowStreamBytes;
     if (hipError_t e = gn::launch_rms_bwd(a, dy_dtype, h_dtype, p, st)) return launch_status(e);
     return dweight ? launch_status(gn::launch_rms_dweight(a.part, parts, H, dweight, w_dtype, st)) : GN_OK;
 }
 
-// The list calls keep small host-side vectors; running out of host memory is answered with
-// a status, as nothing is thrown across the ABI.
 size_t gn_grad_workspace_bytes(const gn_grad_tensor* tensors, int64_t n)
 {
-    return tensors_check(tensors, n, false) ? 0 : size_t(partials_of(tensors, n)) * sizeof(double);
+    return tensors_check(tensors, n, false) ? 0 : size_t(partials_of(tensors, n) + 1) * sizeof(double);
 }
 
 int gn_grad_norm(const gn_grad_tensor* tensors, int64_t n, int norm_type, float* norm,
                  void* workspace, size_t workspace_bytes, void* stream)
 {
-    return grads(tensors, n, norm_type, false, 0.0f, norm, workspace, workspace_bytes, stream);
+    return gn::grads(tensors, n, norm_type, false, 0.0, norm, workspace, workspace_bytes, stream, false);
 }
 
-int gn_grad_clip(const gn_grad_tensor* tensors, int64_t n, int norm_type, float max_norm, float* norm,
+int gn_grad_clip(const gn_grad_tensor* tensors, int64_t n, int norm_type, double max_norm, float* norm,
                  void* workspace, size_t workspace_bytes, void* stream)
 {
-    try {
-        return grads(tensors, n, norm_type, true, max_norm, norm, workspace, workspace_bytes, stream);
-    } catch (const std::bad_alloc&) {
-        return GN_ERR_WORKSPACE;
-    }
+    return gn::grads(tensors, n, norm_type, true, max_norm, norm, workspace, workspace_bytes, stream, false);
 }
 
 }  // extern "C"

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "gn_ops.h"
+#include "gn_ops_internal.hpp"
 
 namespace {
 
@@ -311,8 +312,8 @@ py::tuple grads(const std::vector<at::Tensor>& g, const c10::optional<std::vecto
     if (ws.get_device() != didx || !ws.is_contiguous())
         throw py::value_error("workspace must be a contiguous tensor on the gradients' device");
     const size_t wsb = size_t(ws.numel()) * ws.element_size();
-    const int status = clip ? gn_grad_clip(t.data(), n, norm_type, float(max_norm), np, ws.data_ptr(), wsb, stream_of(didx))
-                            : gn_grad_norm(t.data(), n, norm_type, np, ws.data_ptr(), wsb, stream_of(didx));
+    // The library still looks at norm's pointer, on whose device all tensors have been seen.
+    const int status = gn::grads(t.data(), n, norm_type, clip, max_norm, np, ws.data_ptr(), wsb, stream_of(didx), true);
     if (clip && status == GN_OK)
         for (const at::Tensor& w : out.has_value() ? *out : g)
             if (!w.is_inference()) w.unsafeGetTensorImpl()->bump_version();

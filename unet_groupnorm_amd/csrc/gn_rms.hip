@@ -28,40 +28,60 @@ __device__ __forceinline__ Row row_of(int64_t H, int32_t lanes, int32_t lane)
     return Row{lane, lanes, int32_t(H >> 3), int32_t(H & 7)};
 }
 
-template <typename T, int V, bool EXACT>
-__device__ __forceinline__ void load_row(const T* p, const Row& r, float (&v)[V][8])
-{
-    if constexpr (EXACT) {
-        typename Io<T>::Raw raw[V];
-#pragma unroll
-        for (int u = 0; u < V; ++u) raw[u] = load_any(p + r.vec(u) * 8);
-#pragma unroll
-        for (int u = 0; u < V; ++u) Io<T>::widen(raw[u], v[u]);
-    } else {
-#pragma unroll
-        for (int u = 0; u < V; ++u) {
-            const int32_t i = r.vec(u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] = 0.0f;
-            if (i < r.full)
-                Io<T>::widen(load_any(p + i * 8), v[u]);
-            else if (i == r.full && r.tail)
-                load_part(p + i * 8, r.tail, v[u]);
-        }
-    }
-}
+template <typename T, int V>
+using RawRow = typename Io<T>::Raw[V];
 
-template <typename T, int V, bool EXACT>
-__device__ __forceinline__ void store_row(T* p, const Row& r, const float (&v)[V][8])
+template <typename T, int V, bool EXACT, bool NT>
+__device__ __forceinline__ void load_raw_row(const T* p, const Row& r, RawRow<T, V>& raw)
 {
 #pragma unroll
     for (int u = 0; u < V; ++u) {
         const int32_t i = r.vec(u);
         if (EXACT || i < r.full)
-            store_any(p + i * 8, v[u]);
+            raw[u] = load_any<T, NT>(p + i * 8);
+        else
+            raw[u] = load_part(p + i * 8, i == r.full ? r.tail : 0);
+    }
+}
+
+// A lane's vectors of a row as loaded, zeros behind the row's end; nt (one value for the
+// launch): nontemporal.
+template <typename T, int V, bool EXACT>
+__device__ __forceinline__ void load_raw_row(const T* p, const Row& r, bool nt, RawRow<T, V>& raw)
+{
+    if (nt)
+        load_raw_row<T, V, EXACT, true>(p, r, raw);
+    else
+        load_raw_row<T, V, EXACT, false>(p, r, raw);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void widen_row(const RawRow<T, V>& raw, float (&v)[V][8])
+{
+#pragma unroll
+    for (int u = 0; u < V; ++u) Io<T>::widen(raw[u], v[u]);
+}
+
+template <typename T, int V, bool EXACT, bool NT>
+__device__ __forceinline__ void store_row_as(T* p, const Row& r, const float (&v)[V][8])
+{
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+        const int32_t i = r.vec(u);
+        if (EXACT || i < r.full)
+            store_any<T, NT>(p + i * 8, v[u]);
         else if (i == r.full && r.tail)
             store_part(p + i * 8, r.tail, v[u]);
     }
+}
+
+template <typename T, int V, bool EXACT>
+__device__ __forceinline__ void store_row(T* p, const Row& r, bool nt, const float (&v)[V][8])
+{
+    if (nt)
+        store_row_as<T, V, EXACT, true>(p, r, v);
+    else
+        store_row_as<T, V, EXACT, false>(p, r, v);
 }
 
 // weight as fp32 (ones where it is null).
@@ -74,9 +94,13 @@ __device__ __forceinline__ void load_weight(const void* w, bool f32, const Row& 
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[u][e] = 1.0f;
     } else if (f32) {
-        load_row<float, V, EXACT>(in<float>(w), r, v);
+        RawRow<float, V> raw;
+        load_raw_row<float, V, EXACT, false>(in<float>(w), r, raw);
+        widen_row<float, V>(raw, v);
     } else {
-        load_row<T, V, EXACT>(in<T>(w), r, v);
+        RawRow<T, V> raw;
+        load_raw_row<T, V, EXACT, false>(in<T>(w), r, raw);
+        widen_row<T, V>(raw, v);
     }
 }
 
@@ -131,15 +155,16 @@ __device__ __forceinline__ uint32_t lanes_all(uint32_t v, int32_t lanes)
     return v;
 }
 
-// The result over a whole row for each of its lanes. Rows of several waves meet in s (a word
-// for each wave), in wave order; s is free again once every wave has passed another barrier.
+// The result over a whole row for each of its lanes. The waves of a longer row meet in s (a
+// word for each wave of the row), in wave order; the whole workgroup takes part, and s is free
+// again once every wave has passed another barrier.
 template <typename Op>
-__device__ __forceinline__ uint32_t row_all(uint32_t v, int32_t lanes, uint32_t* s)
+__device__ __forceinline__ uint32_t row_all(uint32_t v, const Row& r, uint32_t* s)
 {
-    v = lanes_all<Op>(v, lanes < 64 ? lanes : 64);
-    if (lanes > 64) {
-        const int nw = lanes >> 6;
-        if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    v = lanes_all<Op>(v, r.lanes < 64 ? r.lanes : 64);
+    if (r.lanes > 64) {
+        const int nw = r.lanes >> 6;
+        if ((r.lane & 63) == 0) s[r.lane >> 6] = v;
         __syncthreads();
         v = s[0];
         for (int w = 1; w < nw; ++w) v = Op::f(v, s[w]);
@@ -147,9 +172,9 @@ __device__ __forceinline__ uint32_t row_all(uint32_t v, int32_t lanes, uint32_t*
     return v;
 }
 
-__device__ __forceinline__ float row_sum(float v, int32_t lanes, uint32_t* s)
+__device__ __forceinline__ float row_sum(float v, const Row& r, uint32_t* s)
 {
-    return __uint_as_float(row_all<AddOp>(__float_as_uint(v), lanes, s));
+    return __uint_as_float(row_all<AddOp>(__float_as_uint(v), r, s));
 }
 
 constexpr int kRowMaxWaves = kRowMaxBlock / 64;
@@ -217,23 +242,28 @@ rms_fwd_kernel(RmsArgs a)
     const int64_t t = int64_t(blockIdx.x) * a.rows + sub;
     if (t >= a.T) return;  // whole rows leave, and with more than 64 lanes whole workgroups
     float h[V][8], w[V][8];
-    load_row<XT, V, EXACT>(in<XT>(a.x) + t * a.x_stride, r, h);
+    RawRow<XT, V> rx;
+    load_raw_row<XT, V, EXACT>(in<XT>(a.x) + t * a.x_stride, r, a.nt, rx);
     if constexpr (kRes) {
         float d[V][8];
-        load_row<HT, V, EXACT>(in<HT>(a.res) + t * a.H, r, d);
+        RawRow<HT, V> rd;
+        load_raw_row<HT, V, EXACT>(in<HT>(a.res) + t * a.H, r, a.nt, rd);
         load_weight<XT, V, EXACT>(a.w, a.w_f32, r, w);
+        widen_row<XT, V>(rx, h);
+        widen_row<HT, V>(rd, d);
 #pragma unroll
         for (int u = 0; u < V; ++u)
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[u][e] = round_to<HT>(h[u][e] + d[u][e]);
-        store_row<HT, V, EXACT>(out<HT>(a.h) + t * a.H, r, h);
+        store_row<HT, V, EXACT>(out<HT>(a.h) + t * a.H, r, a.nt, h);
     } else {
         load_weight<XT, V, EXACT>(a.w, a.w_f32, r, w);
+        widen_row<XT, V>(rx, h);
     }
     float ss = tree_sumsq(h[0]);
 #pragma unroll
     for (int u = 1; u < V; ++u) ss = ss + tree_sumsq(h[u]);
-    ss = row_sum(ss, r.lanes, s_sum);
+    ss = row_sum(ss, r, s_sum);
     const float rstd = 1.0f / sqrtf(ss / float(a.H) + a.eps);
     if (a.rstd && r.lane == 0) a.rstd[t] = rstd;
 #pragma unroll
@@ -242,9 +272,9 @@ rms_fwd_kernel(RmsArgs a)
         for (int e = 0; e < 8; ++e) h[u][e] = h[u][e] * rstd * w[u][e];
     if constexpr (!Q8) {
         if (a.y_f32)
-            store_row<float, V, EXACT>(out<float>(a.y) + t * a.H, r, h);
+            store_row<float, V, EXACT>(out<float>(a.y) + t * a.H, r, a.nt, h);
         else
-            store_row<XT, V, EXACT>(out<XT>(a.y) + t * a.H, r, h);
+            store_row<XT, V, EXACT>(out<XT>(a.y) + t * a.H, r, a.nt, h);
     } else {
         const float qmax = a.q_dtype == GN_Q_INT8 ? 127.0f : 448.0f;
         uint32_t m[V];
@@ -260,7 +290,7 @@ rms_fwd_kernel(RmsArgs a)
         if (a.block == 0) {
 #pragma unroll
             for (int u = 1; u < V; ++u) m[0] = MaxBitsOp::f(m[0], m[u]);
-            m[0] = row_all<MaxBitsOp>(m[0], r.lanes, s_max);
+            m[0] = row_all<MaxBitsOp>(m[0], r, s_max);
         }
 #pragma unroll
         for (int u = 0; u < V; ++u) {
@@ -283,15 +313,17 @@ rms_fwd_kernel(RmsArgs a)
 
 // ------------------------------------------------------------------ backward
 
-// Workgroup b takes the row groups b, b + parts, ...; every lane keeps its columns' sums of
-// dy * xhat in registers over all of them and leaves them in the workspace at the end.
-template <typename DT, typename HT, bool DH, int V, bool EXACT>
-__global__ void __launch_bounds__(kRowMaxBlock)
+// Workgroup b takes the row groups b, b + parts, ... (a.rows rows at once, a.lanes lanes
+// each); the next group's vectors are loaded before this group's are used. Every lane keeps
+// its columns' sums of dy * xhat in registers over all of them; at the end the workgroup adds
+// its rows' sums in LDS and leaves one partial sum for each column in the workspace.
+template <typename DT, typename HT, bool DH, int V, bool EXACT, int BLOCK>
+__global__ void __launch_bounds__(BLOCK)
 rms_bwd_kernel(RmsBwdArgs a)
 {
-    __shared__ uint32_t s_sum[2][kRowMaxWaves];
-    __shared__ float s_dw[256 * 8];
-    const int32_t sub = a.lanes > 64 ? 0 : int32_t(threadIdx.x) / a.lanes;
+    __shared__ uint32_t s_sum[2][BLOCK / 64];
+    __shared__ __align__(16) float s_dw[BLOCK * 8];
+    const int32_t sub = int32_t(threadIdx.x) / a.lanes;
     const Row r = row_of(a.H, a.lanes, int32_t(threadIdx.x) - sub * a.lanes);
     float w[V][8], dw[V][8];
     if (!a.w || a.w_dtype == GN_F32)
@@ -304,29 +336,42 @@ rms_bwd_kernel(RmsBwdArgs a)
     for (int u = 0; u < V; ++u)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[u][e] = 0.0f;
+    RawRow<DT, V> next_dy;
+    RawRow<HT, V> next_h, next_dh;
+    float next_rstd;
+    const auto load = [&](int64_t t) {  // past the last row: the last row again, unused
+        t = t < a.T ? t : a.T - 1;
+        load_raw_row<DT, V, EXACT>(in<DT>(a.dy) + t * a.H, r, a.nt, next_dy);
+        load_raw_row<HT, V, EXACT>(in<HT>(a.h) + t * a.h_stride, r, a.nt, next_h);
+        if constexpr (DH) load_raw_row<HT, V, EXACT>(in<HT>(a.dh) + t * a.H, r, a.nt, next_dh);
+        next_rstd = a.rstd[t];
+    };
     const int64_t groups = (a.T + a.rows - 1) / a.rows;
     int phase = 0;
+    load(int64_t(blockIdx.x) * a.rows + sub);
     for (int64_t g = blockIdx.x; g < groups; g += a.parts, phase ^= 1) {
         const int64_t t = g * a.rows + sub;
-        if (t >= a.T) break;  // only rows of up to 64 lanes, whose sums need no barrier
         float dy[V][8], h[V][8], d[V][8];
-        load_row<DT, V, EXACT>(in<DT>(a.dy) + t * a.H, r, dy);
-        load_row<HT, V, EXACT>(in<HT>(a.h) + t * a.h_stride, r, h);
-        if constexpr (DH) load_row<HT, V, EXACT>(in<HT>(a.dh) + t * a.H, r, d);
-        const float rstd = a.rstd[t];
+        widen_row<DT, V>(next_dy, dy);
+        widen_row<HT, V>(next_h, h);
+        if constexpr (DH) widen_row<HT, V>(next_dh, d);
+        const float rstd = next_rstd;
+        if (g + a.parts < groups) load(t + a.parts * a.rows);
+        const bool row = t < a.T;
         float c = 0.0f;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 h[u][e] = h[u][e] * rstd;
-                dw[u][e] = fmaf(dy[u][e], h[u][e], dw[u][e]);
+                if (row) dw[u][e] = fmaf(dy[u][e], h[u][e], dw[u][e]);
                 dy[u][e] = dy[u][e] * w[u][e];
             }
             c = c + tree_sumprod(dy[u], h[u]);
         }
         if (!a.dx && !a.dres) continue;
-        c = row_sum(c, r.lanes, s_sum[phase]) / float(a.H);
+        c = row_sum(c, r, s_sum[phase] + sub * (r.lanes >> 6)) / float(a.H);
+        if (!row) continue;  // after the row's barrier
 #pragma unroll
         for (int u = 0; u < V; ++u)
 #pragma unroll
@@ -334,53 +379,80 @@ rms_bwd_kernel(RmsBwdArgs a)
                 const float v = rstd * fmaf(-h[u][e], c, dy[u][e]);
                 dy[u][e] = DH ? v + d[u][e] : v;
             }
-        if (a.dres) store_row<HT, V, EXACT>(out<HT>(a.dres) + t * a.H, r, dy);
+        if (a.dres) store_row<HT, V, EXACT>(out<HT>(a.dres) + t * a.H, r, a.nt, dy);
         if (a.dx) {
             if (a.x_dtype == GN_F32)
-                store_row<float, V, EXACT>(out<float>(a.dx) + t * a.H, r, dy);
+                store_row<float, V, EXACT>(out<float>(a.dx) + t * a.H, r, a.nt, dy);
             else if (a.x_dtype == GN_BF16)
-                store_row<uint16_t, V, EXACT>(out<uint16_t>(a.dx) + t * a.H, r, dy);
+                store_row<uint16_t, V, EXACT>(out<uint16_t>(a.dx) + t * a.H, r, a.nt, dy);
             else
-                store_row<_Float16, V, EXACT>(out<_Float16>(a.dx) + t * a.H, r, dy);
+                store_row<_Float16, V, EXACT>(out<_Float16>(a.dx) + t * a.H, r, a.nt, dy);
         }
     }
     if (!a.part) return;
     float* part = a.part + int64_t(blockIdx.x) * a.H;
-    if (a.rows > 1) {  // V == 1: the workgroup's rows, added in their order
+    if (a.rows == 1) {
+        store_row<float, V, EXACT>(part, r, false, dw);
+        return;
+    }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s_dw[threadIdx.x * 8 + e] = dw[0][e];
+    for (int u = 0; u < V; ++u) {
+        if (u) __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_dw[threadIdx.x * 8 + e] = dw[u][e];
         __syncthreads();
-        for (int32_t c = threadIdx.x; c < a.H; c += 256) {
+        const int32_t first = u * a.lanes * 8, n = a.lanes * 8;
+        for (int32_t c = threadIdx.x; c < n && first + c < a.H; c += blockDim.x) {
             float s = s_dw[c];
-            for (int32_t k = 1; k < a.rows; ++k) s = s + s_dw[k * a.lanes * 8 + c];
-            part[c] = s;
+            for (int32_t k = 1; k < a.rows; ++k) s = s + s_dw[k * n + c];
+            part[first + c] = s;
         }
-    } else {
-        store_row<float, V, EXACT>(part, r, dw);
     }
 }
 
-// 64 columns of 4 slices of the parts, each added in order, then the slices in order.
-__global__ void __launch_bounds__(256)
+// A workgroup adds 32 columns of all parts: thread (slice, quad) takes 4 columns of the parts
+// slice, slice + 128, ... in order, and the 128 slices are added in a tree. Bound by one
+// trip to memory, not by bytes: every thread's few loads are in flight together.
+constexpr int kDwBlock = 1024, kDwCols = 32, kDwSlices = kDwBlock / (kDwCols / 4);
+
+__global__ void __launch_bounds__(kDwBlock)
 rms_dweight_kernel(const float* part, int64_t parts, int64_t H, void* dw, int w_dtype)
 {
-    __shared__ float s[4][64];
-    const int col = threadIdx.x & 63, slice = threadIdx.x >> 6;
-    const int64_t c = int64_t(blockIdx.x) * 64 + col;
-    const int64_t n = (parts + 3) / 4, p0 = slice * n, p1 = p0 + n < parts ? p0 + n : parts;
-    float v = 0.0f;
-    if (c < H)
-        for (int64_t p = p0; p < p1; ++p) v = v + part[p * H + c];
-    s[slice][col] = v;
+    __shared__ float s[kDwSlices][kDwCols];
+    const int quad = threadIdx.x & 7, slice = threadIdx.x >> 3;
+    const int64_t c = int64_t(blockIdx.x) * kDwCols + quad * 4;
+    const int n = H - c >= 4 ? 4 : H > c ? int(H - c) : 0;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n == 4) {
+#pragma unroll 8
+        for (int64_t p = slice; p < parts; p += kDwSlices) {
+            const f32x4 q = *reinterpret_cast<const f32x4_any*>(part + p * H + c);
+            v[0] = v[0] + q.x; v[1] = v[1] + q.y; v[2] = v[2] + q.z; v[3] = v[3] + q.w;
+        }
+    } else {
+        for (int64_t p = slice; p < parts; p += kDwSlices)
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (e < n) v[e] = v[e] + part[p * H + c + e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[slice][quad * 4 + e] = v[e];
     __syncthreads();
-    if (slice == 0 && c < H) {
-        v = (s[0][col] + s[1][col]) + (s[2][col] + s[3][col]);
+    for (int half = kDwSlices / 2; half >= 1; half >>= 1) {
+        for (int i = threadIdx.x; i < half * kDwCols; i += kDwBlock) {
+            const int k = i / kDwCols, j = i % kDwCols;
+            s[k][j] = s[k][j] + s[k + half][j];
+        }
+        __syncthreads();
+    }
+    const int64_t col = int64_t(blockIdx.x) * kDwCols + threadIdx.x;
+    if (threadIdx.x < kDwCols && col < H) {
         if (w_dtype == GN_F32)
-            Io<float>::store1(out<float>(dw) + c, v);
+            Io<float>::store1(out<float>(dw) + col, s[0][threadIdx.x]);
         else if (w_dtype == GN_BF16)
-            Io<uint16_t>::store1(out<uint16_t>(dw) + c, v);
+            Io<uint16_t>::store1(out<uint16_t>(dw) + col, s[0][threadIdx.x]);
         else
-            Io<_Float16>::store1(out<_Float16>(dw) + c, v);
+            Io<_Float16>::store1(out<_Float16>(dw) + col, s[0][threadIdx.x]);
     }
 }
 
@@ -453,13 +525,17 @@ hipError_t fwd(const RmsArgs& a, bool q8, const RowPlan& p, hipStream_t st)
 }
 
 template <typename DT, typename HT>
-hipError_t bwd(const RmsBwdArgs& a, const RowPlan& p, hipStream_t st)
+hipError_t bwd(const RmsBwdArgs& a, const BwdPlan& p, hipStream_t st)
 {
     return with_row(p, [&](auto v, auto exact) {
         constexpr int V = decltype(v)::value;
         constexpr bool E = decltype(exact)::value;
-        return a.dh ? launch(rms_bwd_kernel<DT, HT, true, V, E>, dim3(unsigned(a.parts)), dim3(p.block), st, a)
-                    : launch(rms_bwd_kernel<DT, HT, false, V, E>, dim3(unsigned(a.parts)), dim3(p.block), st, a);
+        const dim3 grid = dim3(unsigned(a.parts)), block = dim3(p.block);
+        if (p.block <= 512)
+            return a.dh ? launch(rms_bwd_kernel<DT, HT, true, V, E, 512>, grid, block, st, a)
+                        : launch(rms_bwd_kernel<DT, HT, false, V, E, 512>, grid, block, st, a);
+        return a.dh ? launch(rms_bwd_kernel<DT, HT, true, V, E, 1024>, grid, block, st, a)
+                    : launch(rms_bwd_kernel<DT, HT, false, V, E, 1024>, grid, block, st, a);
     });
 }
 
@@ -476,7 +552,7 @@ hipError_t launch_rms_fwd(const RmsArgs& a, int x_dtype, int r_dtype, bool q8, c
     return r_dtype == GN_F32 ? fwd<_Float16, float>(a, q8, p, st) : fwd<_Float16, _Float16>(a, q8, p, st);
 }
 
-hipError_t launch_rms_bwd(const RmsBwdArgs& a, int dy_dtype, int h_dtype, const RowPlan& p, hipStream_t st)
+hipError_t launch_rms_bwd(const RmsBwdArgs& a, int dy_dtype, int h_dtype, const BwdPlan& p, hipStream_t st)
 {
     if (h_dtype == GN_BF16)
         return dy_dtype == GN_F32 ? bwd<float, uint16_t>(a, p, st) : bwd<uint16_t, uint16_t>(a, p, st);
@@ -489,7 +565,7 @@ hipError_t launch_rms_bwd(const RmsBwdArgs& a, int dy_dtype, int h_dtype, const 
 
 hipError_t launch_rms_dweight(const float* part, int64_t parts, int64_t H, void* dw, int w_dtype, hipStream_t st)
 {
-    return launch(rms_dweight_kernel, dim3(unsigned((H + 63) / 64)), dim3(256), st, part, parts, H, dw, w_dtype);
+    return launch(rms_dweight_kernel, dim3(unsigned((H + kDwCols - 1) / kDwCols)), dim3(kDwBlock), st, part, parts, H, dw, w_dtype);
 }
 
 hipError_t launch_q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, int64_t H, int64_t block,
