@@ -4,7 +4,8 @@ libgn_probe.so, the measurement kernels that the benchmark and the tests use bes
 libgn.so: the C ABI (csrc/gn_api.cpp), the launch plans (csrc/gn_plan.cpp) and the kernels
 (csrc/gn_kernels.hip for NCDHW, csrc/gn_kernels_cl.hip for channels-last,
 csrc/gn_kernels_shard.hip for spatial shards), and beside them the row norm and the
-gradient list (csrc/gn_ops_api.cpp, csrc/gn_rms.hip, csrc/gn_grad.hip); compiled with hipcc
+gradient list (csrc/gn_ops_api.cpp, csrc/gn_rms.hip, csrc/gn_rms_bwd.hip,
+csrc/gn_grad.hip); compiled with hipcc
 one source at a time in parallel, then linked into ``unet_groupnorm_amd/libgn.so``.
 
 _gnbind (csrc/gn_binding.cpp and csrc/gn_ops_binding.cpp, a Python extension module linked
@@ -30,7 +31,7 @@ LIB = os.path.join(HERE, "libgn.so")
 PROBE_LIB = os.path.join(HERE, "libgn_probe.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["gn_plan.cpp", "gn_api.cpp", "gn_kernels.hip", "gn_kernels_cl.hip", "gn_kernels_shard.hip",
-           "gn_ops_api.cpp", "gn_rms.hip", "gn_grad.hip"]
+           "gn_ops_api.cpp", "gn_rms.hip", "gn_rms_bwd.hip", "gn_grad.hip"]
 PROBE_SOURCES = ["probe_kernels.hip"]
 BIND_SOURCES = ["gn_binding.cpp", "gn_ops_binding.cpp"]
 BIND_NAME = "_gnbind"

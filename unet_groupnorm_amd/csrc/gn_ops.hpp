@@ -11,38 +11,38 @@ namespace gn {
 
 // ------------------------------------------------------------------ row norm
 
-// How a row of H columns is laid over lanes: `lanes` lanes hold one row, each `vecs` vectors
-// of 8 columns (vector v belongs to lane v mod lanes); lanes is a power of two up to 64 with
-// 256 / lanes rows in a workgroup, or a multiple of 64 with one row in a workgroup. A pure
-// function of H, so a row's sums are taken in the same order whatever T is.
+// How a row of H columns is laid over lanes: in pieces of `width` columns, 4 where an fp32
+// tensor is streamed (16 bytes a lane) and 8 where all are 16-bit. `lanes` lanes hold one row,
+// each `vecs` pieces (piece v belongs to lane v mod lanes); lanes is a power of two up to 64
+// with 256 / lanes rows in a workgroup, or a multiple of 64 with one row in a workgroup. A pure
+// function of H and the types, so a row's sums are taken in the same order whatever T is.
 struct RowPlan {
-    int32_t lanes, vecs;
+    int32_t width, lanes, vecs;
     int32_t block, rows;  // threads and rows of a workgroup
-    bool exact;           // every lane's vectors are whole and inside the row
+    bool exact;           // every lane's pieces are whole and inside the row
 };
 
-// Largest number of vectors a lane holds, and of threads in a workgroup.
-constexpr int kRowMaxVecs = 4;
 constexpr int kRowMaxBlock = 1024;
-static_assert(int64_t(kRowMaxVecs) * kRowMaxBlock * 8 == GN_RMS_MAX_COLUMNS, "widest row");
+static_assert(int64_t(kRowMaxBlock) * 4 * 8 == GN_RMS_MAX_COLUMNS, "widest row: 4 pieces of 8, or 8 of 4");
 
-inline RowPlan row_plan(int64_t H)
+inline RowPlan row_plan(int64_t H, bool fp32)
 {
-    const int64_t nv = (H + 7) / 8;
     RowPlan p;
-    if (nv <= 64) {
+    p.width = fp32 ? 4 : 8;
+    const int64_t n = (H + p.width - 1) / p.width;
+    if (n <= 64) {
         p.lanes = 1;
-        while (p.lanes < nv) p.lanes *= 2;
+        while (p.lanes < n) p.lanes *= 2;
         p.vecs = 1;
         p.block = 256;
         p.rows = 256 / p.lanes;
     } else {
-        p.vecs = nv <= 256 ? 1 : nv <= 1024 ? 2 : 4;
-        p.lanes = int32_t(((nv + p.vecs - 1) / p.vecs + 63) / 64 * 64);
+        p.vecs = n <= 256 ? 1 : n <= 1024 ? 2 : n <= 2048 || !fp32 ? 4 : 8;
+        p.lanes = int32_t(((n + p.vecs - 1) / p.vecs + 63) / 64 * 64);
         p.block = p.lanes;
         p.rows = 1;
     }
-    p.exact = int64_t(p.lanes) * p.vecs * 8 == H;
+    p.exact = int64_t(p.lanes) * p.vecs * p.width == H;
     return p;
 }
 
@@ -57,10 +57,10 @@ struct BwdPlan : RowPlan {
 constexpr int kBwdBlock = 512;
 constexpr int64_t kBwdParts = 256;
 
-inline BwdPlan bwd_plan(int64_t T, int64_t H)
+inline BwdPlan bwd_plan(int64_t T, int64_t H, bool fp32)
 {
     BwdPlan p;
-    static_cast<RowPlan&>(p) = row_plan(H);
+    static_cast<RowPlan&>(p) = row_plan(H, fp32);
     const int32_t least = p.lanes < 64 ? 64 / p.lanes : 1;  // rows of a whole wave
     int64_t rows = kBwdBlock / p.lanes;
     while (rows > least && (T + rows - 1) / rows < kBwdParts) rows /= 2;
@@ -71,7 +71,7 @@ inline BwdPlan bwd_plan(int64_t T, int64_t H)
     return p;
 }
 
-// Calls that move more than this many bytes take their rows with nontemporal accesses.
+// Calls that move more than this many bytes load their rows nontemporally.
 constexpr int64_t kRowStreamBytes = int64_t(160) << 20;
 
 struct RmsArgs {
@@ -84,11 +84,11 @@ struct RmsArgs {
     float* scale;
     int64_t T, H, x_stride;
     float eps;
-    int32_t w_f32, y_f32;     // weight and y in fp32 (else x's dtype); weight may be null
+    int32_t w_dtype, y_f32;   // weight's gn_dtype (it may be null); y in fp32, else in x's dtype
     int32_t lanes, rows;
     int32_t q_dtype, block;   // 8-bit output: format, columns of a scale (0: the row)
     int64_t scales;           // scales of a row
-    bool nt;                  // nontemporal loads and stores of the rows
+    bool nt;                  // nontemporal loads of the rows
 };
 
 struct RmsBwdArgs {
@@ -103,7 +103,7 @@ struct RmsBwdArgs {
     int64_t T, H, h_stride, parts;
     int32_t w_dtype, x_dtype;  // gn_dtype codes
     int32_t lanes, rows;
-    bool nt;                   // nontemporal loads and stores of the rows
+    bool nt;                   // nontemporal loads of the rows
 };
 
 hipError_t launch_rms_fwd(const RmsArgs& a, int x_dtype, int r_dtype, bool q8, const RowPlan& p, hipStream_t st);

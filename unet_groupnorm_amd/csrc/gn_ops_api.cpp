@@ -145,13 +145,14 @@ int forward(const void* x, int x_dtype, int64_t x_stride, const void* res, int r
         return GN_ERR_OVERLAP;
     OnDeviceOf dev;
     if ((rc = dev.enter(x, stream)) || (rc = dev.holds({res, w, y, h, rstd, scale}))) return rc;
-    const gn::RowPlan p = gn::row_plan(H);
+    const gn::RowPlan p =
+        gn::row_plan(H, x_dtype == GN_F32 || (res && r_dtype == GN_F32) || (!q8 && y_dtype == GN_F32));
     gn::RmsArgs a{};
     a.w = w;
     a.H = H;
     a.x_stride = x_stride;
     a.eps = eps;
-    a.w_f32 = w_dtype == GN_F32;
+    a.w_dtype = w_dtype;
     a.y_f32 = y_dtype == GN_F32;
     a.lanes = p.lanes;
     a.rows = p.rows;
@@ -389,7 +390,9 @@ int gn_q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, 
 size_t gn_rms_workspace_bytes(int64_t T, int64_t H)
 {
     if (rows_check(T, H, H)) return 0;
-    return size_t(std::max<int64_t>(gn::bwd_plan(T, H).parts, 1)) * size_t(H) * sizeof(float);
+    // whichever the types will be
+    const int64_t parts = std::max(gn::bwd_plan(T, H, false).parts, gn::bwd_plan(T, H, true).parts);
+    return size_t(std::max<int64_t>(parts, 1)) * size_t(H) * sizeof(float);
 }
 
 int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, int64_t h_stride,
@@ -420,7 +423,7 @@ int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, in
         !aligned(weight, size_of(w_dtype)) || !aligned(dh, size_of(h_dtype)) || !aligned(dx, size_of(x_dtype)) ||
         !aligned(dres, size_of(h_dtype)))
         return GN_ERR_ALIGN;
-    const gn::BwdPlan p = gn::bwd_plan(T, H);
+    const gn::BwdPlan p = gn::bwd_plan(T, H, dy_dtype == GN_F32 || h_dtype == GN_F32);
     const int64_t parts = p.parts;
     const Span sy(dy, T * H * size_of(dy_dtype)), sh(h, rows_bytes(T, H, h_stride, h_dtype)), ss(rstd, T * 4),
         sw(weight, H * size_of(w_dtype)), sd(dh, T * H * size_of(h_dtype)), ox(dx, T * H * size_of(x_dtype)),
