@@ -76,6 +76,17 @@ struct Piece {
                 w[e] = Io<_Float16>::pack(v[2 * e], v[2 * e + 1]);
         }
     }
+    // The words become unknown to the compiler, which then widens them anew instead of keeping
+    // what it widened before.
+    __device__ __forceinline__ void forget()
+    {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            uint32_t x = w[k];
+            asm volatile("" : "+v"(x));
+            w[k] = x;
+        }
+    }
     template <bool NT>
     __device__ __forceinline__ void store(T* p) const
     {
@@ -86,17 +97,19 @@ struct Piece {
         else
             *q = t;
     }
-    __device__ __forceinline__ void store_part(T* p, int n) const
+    __device__ __forceinline__ void store_part(T* p, int n) const { store_some(p, 0, n); }
+    // Elements lo to hi - 1.
+    __device__ __forceinline__ void store_some(T* p, int lo, int hi) const
     {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int e = 0; e < W; ++e)
-                if (e < n) p[e] = __uint_as_float(w[e]);
+                if (e >= lo && e < hi) p[e] = __uint_as_float(w[e]);
         } else {
             uint16_t* q = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
             for (int e = 0; e < W; ++e)
-                if (e < n) q[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
+                if (e >= lo && e < hi) q[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
         }
     }
 };

@@ -23,6 +23,8 @@ struct RowPlan {
 };
 
 constexpr int kRowMaxBlock = 1024;
+// Threads of a workgroup over rows of up to 64 lanes.
+constexpr int kShortBlock = 256;
 static_assert(int64_t(kRowMaxBlock) * 4 * 8 == GN_RMS_MAX_COLUMNS, "widest row: 4 pieces of 8, or 8 of 4");
 
 inline RowPlan row_plan(int64_t H, bool fp32)
@@ -34,8 +36,8 @@ inline RowPlan row_plan(int64_t H, bool fp32)
         p.lanes = 1;
         while (p.lanes < n) p.lanes *= 2;
         p.vecs = 1;
-        p.block = 256;
-        p.rows = 256 / p.lanes;
+        p.block = kShortBlock;
+        p.rows = kShortBlock / p.lanes;
     } else {
         p.vecs = n <= 256 ? 1 : n <= 1024 ? 2 : n <= 2048 || !fp32 ? 4 : 8;
         p.lanes = int32_t(((n + p.vecs - 1) / p.vecs + 63) / 64 * 64);
@@ -71,8 +73,11 @@ inline BwdPlan bwd_plan(int64_t T, int64_t H, bool fp32)
     return p;
 }
 
-// Calls that move more than this many bytes load their rows nontemporally.
-constexpr int64_t kRowStreamBytes = int64_t(160) << 20;
+// Calls that move more than this many bytes load their rows nontemporally. Measured, plain
+// against nontemporal, on inputs that the last-level cache may still hold in part: forward of
+// 2048 x 4096 bf16 (64 MiB) 11.2 and 13.3 us, 8192 x 4096 (256 MiB) 41.8 and 42.1, 16384 x 4096
+// (512 MiB) 92.7 and 78.4; backward of 8192 x 4096 bf16 49.4 and 48.2, fp32 (512 MiB) 99 and 86.
+constexpr int64_t kRowStreamBytes = int64_t(200) << 20;
 
 struct RmsArgs {
     const void* x;
@@ -83,7 +88,7 @@ struct RmsArgs {
     float* rstd;
     float* scale;
     int64_t T, H, x_stride;
-    float eps;
+    float eps, inv_H;
     int32_t w_dtype, y_f32;   // weight's gn_dtype (it may be null); y in fp32, else in x's dtype
     int32_t lanes, rows;
     int32_t q_dtype, block;   // 8-bit output: format, columns of a scale (0: the row)
@@ -97,12 +102,13 @@ struct RmsBwdArgs {
     const void* w;
     const void* dh;
     const float* rstd;
-    void* dx;
-    void* dres;
+    void* d;       // the gradient in h's type (null: none)
+    void* dx;      // once more, in x's type (null: none)
     float* part;   // [parts][H], null: no weight gradient
     int64_t T, H, h_stride, parts;
     int32_t w_dtype, x_dtype;  // gn_dtype codes
     int32_t lanes, rows;
+    float inv_H;
     bool nt;                   // nontemporal loads of the rows
 };
 

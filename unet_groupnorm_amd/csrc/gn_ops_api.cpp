@@ -152,6 +152,7 @@ int forward(const void* x, int x_dtype, int64_t x_stride, const void* res, int r
     a.H = H;
     a.x_stride = x_stride;
     a.eps = eps;
+    a.inv_H = 1.0f / float(H);
     a.w_dtype = w_dtype;
     a.y_f32 = y_dtype == GN_F32;
     a.lanes = p.lanes;
@@ -448,8 +449,9 @@ int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, in
     a.w = weight;
     a.dh = dh;
     a.rstd = rstd;
-    a.dx = dx;
-    a.dres = dres;
+    // one output in h's type, and a second where the types differ or both are asked for
+    a.d = dres ? dres : x_dtype == h_dtype ? dx : nullptr;
+    a.dx = a.d == dx ? nullptr : dx;
     a.part = dweight ? static_cast<float*>(workspace) : nullptr;
     a.T = T;
     a.H = H;
@@ -459,6 +461,7 @@ int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, in
     a.x_dtype = x_dtype;
     a.lanes = p.lanes;
     a.rows = p.rows;
+    a.inv_H = 1.0f / float(H);
     a.nt = T * H * (size_of(dy_dtype) + size_of(h_dtype) * (dh ? 2 : 1) + (dx ? size_of(x_dtype) : 0) +
                     (dres ? size_of(h_dtype) : 0)) > gn::kRowStreamBytes;
     if (hipError_t e = gn::launch_rms_bwd(a, dy_dtype, h_dtype, p, st)) return launch_status(e);

@@ -4,6 +4,7 @@
 // Argument marshalling only: every tensor is checked (device, dtype, sizes, layout), outputs
 // not given are allocated on the first tensor's device, that device's current HIP stream is
 // taken from torch, and the C ABI is called; its status is returned with the outputs.
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPStream.h>
 #include <hip/hip_runtime.h>
 #include <torch/csrc/autograd/variable.h>
@@ -106,6 +107,14 @@ float* f32(const char* name, const at::Tensor& t, int64_t n, int didx)
     return static_cast<float*>(t.data_ptr());
 }
 
+// A new contiguous tensor on x's device. On a GPU this goes to the allocator without torch's
+// dispatcher, which small calls would feel (three outputs: 3.1 us against 1.9).
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& x)
+{
+    if (x.is_cuda()) return at::Tensor(at::detail::empty_cuda(sizes, type, x.device(), c10::nullopt));
+    return at::empty(sizes, x.options().dtype(type));
+}
+
 py::object or_none(const at::Tensor& t) { return t.defined() ? py::cast(t) : py::none(); }
 
 // The sizes of x without its last dimension, and with n in its place where n >= 0.
@@ -145,7 +154,7 @@ at::Tensor h_of(const at::Tensor& x, const OptTensor& residual, const OptTensor&
         if (h.has_value()) throw py::value_error("h is an output of a call with a residual");
         return x;
     }
-    if (!h.has_value()) return at::empty_like(*residual);
+    if (!h.has_value()) return fresh(residual->sizes(), residual->scalar_type(), *residual);
     like("h", *h, x);
     if (h->scalar_type() != residual->scalar_type()) throw py::type_error("h must have residual's dtype");
     return *h;
@@ -154,7 +163,7 @@ at::Tensor h_of(const at::Tensor& x, const OptTensor& residual, const OptTensor&
 at::Tensor rstd_of(const at::Tensor& x, const OptTensor& rstd, bool need)
 {
     if (rstd.has_value()) return *rstd;
-    return need ? at::empty(lead(x), x.options().dtype(at::kFloat)) : at::Tensor();
+    return need ? fresh(lead(x), at::kFloat, x) : at::Tensor();
 }
 
 py::tuple rms_forward(const at::Tensor& x, const OptTensor& weight, double eps, const OptTensor& residual,
@@ -162,8 +171,7 @@ py::tuple rms_forward(const at::Tensor& x, const OptTensor& weight, double eps, 
                       const OptTensor& rstd_out)
 {
     const Inputs in = inputs_of(x, weight, residual);
-    const at::Tensor y = out.has_value() ? *out : at::empty(x.sizes(), x.options().dtype(
-                                                      out_code < 0 ? x.scalar_type() : type_of_code(out_code)));
+    const at::Tensor y = out.has_value() ? *out : fresh(x.sizes(), out_code < 0 ? x.scalar_type() : type_of_code(out_code), x);
     void* yp = like("out", y, x);
     const int yc = code_of(y, "out");
     const at::Tensor h = h_of(x, residual, h_out), rstd = rstd_of(x, rstd_out, need_rstd);
@@ -181,12 +189,11 @@ py::tuple rms_forward_q8(const at::Tensor& x, const OptTensor& weight, double ep
     const Inputs in = inputs_of(x, weight, residual);
     const at::Tensor q = out.has_value()
                              ? *out
-                             : at::empty(x.sizes(), x.options().dtype(q_dtype == GN_Q_INT8 ? at::kChar
-                                                                                           : at::kFloat8_e4m3fn));
+                             : fresh(x.sizes(), q_dtype == GN_Q_INT8 ? at::kChar : at::kFloat8_e4m3fn, x);
     void* qp = like("out", q, x);
     const int qc = q_code_of(q);
     const int64_t n = scales_of(in.r.H, block);
-    const at::Tensor scale = scale_out.has_value() ? *scale_out : at::empty(lead(x, n), x.options().dtype(at::kFloat));
+    const at::Tensor scale = scale_out.has_value() ? *scale_out : fresh(lead(x, n), at::kFloat, x);
     float* sp = f32("scale", scale, in.r.T * n, in.didx);
     const at::Tensor h = h_of(x, residual, h_out), rstd = rstd_of(x, rstd_out, need_rstd);
     float* rp = rstd.defined() ? f32("rstd", rstd, in.r.T, in.didx) : nullptr;
@@ -203,7 +210,7 @@ py::tuple q8_dequantize(const at::Tensor& q, const at::Tensor& scale, int out_co
     if (!q.is_contiguous()) throw py::value_error("q must be contiguous");
     const int qc = q_code_of(q), didx = q.get_device();
     const at::Tensor o =
-        out.has_value() ? *out : at::empty(q.sizes(), q.options().dtype(type_of_code(out_code < 0 ? GN_F32 : out_code)));
+        out.has_value() ? *out : fresh(q.sizes(), type_of_code(out_code < 0 ? GN_F32 : out_code), q);
     void* op = like("out", o, q);
     const int oc = code_of(o, "out");
     const int status = gn_q8_dequantize(q.data_ptr(), qc, f32("scale", scale, r.T * scales_of(r.H, block), didx), r.T,
@@ -233,19 +240,19 @@ py::tuple rms_backward(const at::Tensor& dy, const at::Tensor& h, const at::Tens
     }
     at::Tensor dx, dres, dw;
     if (need_dx) {
-        dx = dx_out.has_value() ? *dx_out : at::empty(h.sizes(), h.options().dtype(type_of_code(xc)));
+        dx = dx_out.has_value() ? *dx_out : fresh(h.sizes(), type_of_code(xc), h);
         like("dx", dx, h);
         if (code_of(dx, "dx") != xc) throw py::type_error("dx must have x's dtype");
     }
     if (need_dres) {
         // one tensor is both gradients where the dtypes agree
         if (dres_out.has_value()) dres = *dres_out;
-        else dres = need_dx && xc == hc ? dx : at::empty(h.sizes(), h.options());
+        else dres = need_dx && xc == hc ? dx : fresh(h.sizes(), h.scalar_type(), h);
         like("dres", dres, h);
         if (dres.scalar_type() != h.scalar_type()) throw py::type_error("dres must have h's dtype");
     }
     if (need_dweight) {
-        dw = dweight_out.has_value() ? *dweight_out : at::empty({r.H}, h.options().dtype(type_of_code(wc)));
+        dw = dweight_out.has_value() ? *dweight_out : fresh({r.H}, type_of_code(wc), h);
         vec("dweight", dw, r.H, didx);
         if (code_of(dw, "dweight") != wc) throw py::type_error("dweight must have weight's dtype");
     }
@@ -254,7 +261,7 @@ py::tuple rms_backward(const at::Tensor& dy, const at::Tensor& h, const at::Tens
     size_t wsb = 0;
     if (need_dweight) {
         ws = workspace.has_value() ? *workspace
-                                   : at::empty({int64_t(gn_rms_workspace_bytes(r.T, r.H))}, h.options().dtype(at::kByte));
+                                   : fresh({int64_t(gn_rms_workspace_bytes(r.T, r.H))}, at::kByte, h);
         if (ws.get_device() != didx || !ws.is_contiguous())
             throw py::value_error("workspace must be a contiguous tensor on h's device");
         wsp = ws.data_ptr();
@@ -303,12 +310,11 @@ py::tuple grads(const std::vector<at::Tensor>& g, const c10::optional<std::vecto
             t[i].out_dtype = code_of(o, "out");
         }
     }
-    const at::Tensor norm = norm_out.has_value() ? *norm_out : at::empty({}, g[0].options().dtype(at::kFloat));
+    const at::Tensor norm = norm_out.has_value() ? *norm_out : fresh({}, at::kFloat, g[0]);
     float* np = f32("norm", norm, 1, didx);
     const int64_t n = int64_t(t.size());
     const at::Tensor ws = workspace.has_value() ? *workspace
-                                                : at::empty({int64_t(gn_grad_workspace_bytes(t.data(), n))},
-                                                            g[0].options().dtype(at::kByte));
+                                                : fresh({int64_t(gn_grad_workspace_bytes(t.data(), n))}, at::kByte, g[0]);
     if (ws.get_device() != didx || !ws.is_contiguous())
         throw py::value_error("workspace must be a contiguous tensor on the gradients' device");
     const size_t wsb = size_t(ws.numel()) * ws.element_size();

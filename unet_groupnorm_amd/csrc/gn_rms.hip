@@ -19,24 +19,58 @@ constexpr int kRowMaxWaves = kRowMaxBlock / 64;
 
 constexpr float kQMin = 0x1p-126f;  // smallest scale, the smallest normal fp32
 
-// 4 quotients, |v| <= qmax, to 4 bytes: nearest, ties to even.
-__device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, int q_dtype)
+struct Scaled {
+    float scale, inv;
+};
+
+// The scale of a run whose largest magnitude has the bits `amax`: a NaN and no factor where
+// that is a NaN or an infinity.
+__device__ __forceinline__ Scaled scale_of(uint32_t amax, int q_dtype)
 {
-    if (q_dtype == GN_Q_INT8)
-        return (uint32_t(int32_t(rintf(a))) & 0xffu) | ((uint32_t(int32_t(rintf(b))) & 0xffu) << 8) |
-               ((uint32_t(int32_t(rintf(c))) & 0xffu) << 16) | (uint32_t(int32_t(rintf(d))) << 24);
-    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
+    if (amax >= 0x7f800000u) return Scaled{__uint_as_float(0x7fc00000u), 0.0f};
+    const float s = fmaxf(__uint_as_float(amax) / (q_dtype == GN_Q_INT8 ? 127.0f : 448.0f), kQMin);
+    return Scaled{s, 1.0f / s};
 }
 
-// W (4 or 8) quotients to n of their W bytes.
+// Bits of the largest magnitude of a piece. The comparison is that of integers, which orders
+// a NaN above all numbers.
 template <int W>
-__device__ __forceinline__ void store_q(uint8_t* p, int n, const float (&v)[W], int q_dtype)
+__device__ __forceinline__ uint32_t piece_amax(const float (&v)[W])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < W; ++e) m = MaxBitsOp::f(m, __float_as_uint(v[e]) & 0x7fffffffu);
+    return m;
+}
+
+// 4 values times inv, |v * inv| <= qmax, to 4 bytes: nearest, ties to even. For int8 the
+// product is added to 1.5 * 2^23 in one rounding, which leaves the integer in the sum's low
+// bits; a NaN (of a run that holds one, or an infinity) becomes 0 in both formats.
+__device__ __forceinline__ uint32_t quantize4(const float* v, Scaled sc, int q_dtype)
+{
+    uint32_t q;
+    if (q_dtype == GN_Q_INT8) {
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(fmaf(v[e], sc.inv, 0x1.8p23f));
+        // byte 0 of each, first value lowest
+        q = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
+                                  __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
+    } else {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * sc.inv, v[1] * sc.inv, 0, false);
+        q = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[2] * sc.inv, v[3] * sc.inv, lo, true));
+    }
+    return sc.scale == sc.scale ? q : 0u;
+}
+
+// W (4 or 8) values times inv to their bytes lo to hi - 1.
+template <int W>
+__device__ __forceinline__ void store_q(uint8_t* p, int lo, int hi, const float (&v)[W], Scaled sc, int q_dtype)
 {
     uint32_t q[W / 4];
 #pragma unroll
-    for (int k = 0; k < W / 4; ++k) q[k] = quantize4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], q_dtype);
-    if (n >= W) {
+    for (int k = 0; k < W / 4; ++k) q[k] = quantize4(v + 4 * k, sc, q_dtype);
+    if (lo == 0 && hi == W) {
         typedef uint32_t WordsAny __attribute__((ext_vector_type(W / 4), aligned(1)));
         WordsAny t;
 #pragma unroll
@@ -44,26 +78,36 @@ __device__ __forceinline__ void store_q(uint8_t* p, int n, const float (&v)[W], 
         *reinterpret_cast<WordsAny*>(p) = t;
     } else {
 #pragma unroll
-        for (int e = 0; e < W - 1; ++e)
-            if (e < n) p[e] = uint8_t((q[e / 4] >> (8 * (e & 3))) & 0xffu);
+        for (int e = 0; e < W; ++e)
+            if (e >= lo && e < hi) p[e] = uint8_t((q[e / 4] >> (8 * (e & 3))) & 0xffu);
     }
-}
-
-struct Scaled {
-    float scale, inv;
-};
-
-// The scale of a run whose largest magnitude has the bits `amax`.
-__device__ __forceinline__ Scaled scale_of(uint32_t amax, float qmax)
-{
-    if (amax >= 0x7f800000u) return Scaled{__uint_as_float(0x7fc00000u), 0.0f};
-    const float s = fmaxf(__uint_as_float(amax) / qmax, kQMin);
-    return Scaled{s, 1.0f / s};
 }
 
 // ------------------------------------------------------------------ forward
 
-template <typename XT, typename RT, int W, int V, bool EXACT, bool Q8>
+// One piece's output in 8 bits; `share` lanes share the scale, and the first of them stores it.
+template <int W, int END>
+__device__ __forceinline__ void store_q8(const RmsArgs& a, const Row<W>& r, int64_t t, int32_t i, int32_t share,
+                                         Scaled sc, const float (&v)[W])
+{
+    if (END != kExact && (i > r.full || (i == r.full && !r.tail))) return;
+    const bool whole = END == kExact || i < r.full;
+    store_q<W>(out<uint8_t>(a.y) + t * a.H + (whole ? i * W : r.column(i)), whole || END == kTiny ? 0 : W - r.tail,
+               whole || END == kEnds ? W : r.H, v, sc, a.q_dtype);
+    if (a.block == 0 ? i == 0 : i % share == 0) a.scale[t * a.scales + (a.block == 0 ? 0 : i / share)] = sc.scale;
+}
+
+// Lanes that share a scale: the row's, or block / W neighbours (a row of fewer lanes than that
+// is one run).
+template <int W>
+__device__ __forceinline__ int32_t lanes_of_scale(const RmsArgs& a, const Row<W>& r)
+{
+    return a.block == 0 || a.block / W >= r.lanes ? r.lanes : a.block / W;
+}
+
+// Outputs are written after the sum's barrier: an output may take an input's place, and lanes
+// at the row's end read columns of others.
+template <typename XT, typename RT, int W, int V, int END, bool Q8>
 __global__ void __launch_bounds__(kRowMaxBlock)
 rms_fwd_kernel(RmsArgs a)
 {
@@ -75,71 +119,61 @@ rms_fwd_kernel(RmsArgs a)
     const int64_t t = int64_t(blockIdx.x) * a.rows + sub;
     if (t >= a.T) return;  // whole rows leave, and with more than 64 lanes whole workgroups
     float h[V][W], w[V][W];
+    Piece<HT, W> rd[kRes ? V : 1];
     Piece<XT, W> rx[V];
-    load_row<XT, W, V, EXACT>(in<XT>(a.x) + t * a.x_stride, r, a.nt, rx);
-    if constexpr (kRes) {
-        float d[V][W];
-        Piece<HT, W> rd[V];
-        load_row<HT, W, V, EXACT>(in<HT>(a.res) + t * a.H, r, a.nt, rd);
-        load_weight<W, V, EXACT>(a.w, a.w_dtype, r, w);
-        widen_row<XT, W, V>(rx, h);
-        widen_row<HT, W, V>(rd, d);
+    load_row<XT, W, V, END>(in<XT>(a.x) + t * a.x_stride, r, a.nt, rx);
+    if constexpr (kRes) load_row<HT, W, V, END>(in<HT>(a.res) + t * a.H, r, a.nt, rd);
 #pragma unroll
-        for (int u = 0; u < V; ++u)
+    for (int u = 0; u < V; ++u) load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[u]);
+    float ss = 0.0f;
 #pragma unroll
-            for (int e = 0; e < W; ++e) h[u][e] = round_to<HT>(h[u][e] + d[u][e]);
-        store_row<HT, W, V, EXACT>(out<HT>(a.h) + t * a.H, r, h);
-    } else {
-        load_weight<W, V, EXACT>(a.w, a.w_dtype, r, w);
-        widen_row<XT, W, V>(rx, h);
+    for (int u = 0; u < V; ++u) {
+        widen_piece<XT, W, END>(rx[u], r, r.piece(u), h[u]);
+        if constexpr (kRes) {  // the sum rounded to the residual's type, and taken as stored
+            float d[W];
+            widen_piece<HT, W, END>(rd[u], r, r.piece(u), d);
+#pragma unroll
+            for (int e = 0; e < W; ++e) d[e] = h[u][e] + d[e];
+            rd[u].narrow(d);
+            rd[u].widen(h[u]);
+        }
+        ss = ss + tree_sumsq(h[u]);
     }
-    float ss = tree_sumsq(h[0]);
+    ss = V > 1 || r.lanes > 64 ? row_sum<true>(ss, r, s_sum) : row_sum<false>(ss, r, s_sum);
+    if constexpr (kRes) {
 #pragma unroll
-    for (int u = 1; u < V; ++u) ss = ss + tree_sumsq(h[u]);
-    ss = row_sum(ss, r, s_sum);
-    const float rstd = 1.0f / sqrtf(ss / float(a.H) + a.eps);
+        for (int u = 0; u < V; ++u) store_values<HT, W, END>(out<HT>(a.h) + t * a.H, r, r.piece(u), h[u]);
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(ss, a.inv_H, a.eps));
     if (a.rstd && r.lane == 0) a.rstd[t] = rstd;
 #pragma unroll
     for (int u = 0; u < V; ++u)
 #pragma unroll
         for (int e = 0; e < W; ++e) h[u][e] = h[u][e] * rstd * w[u][e];
     if constexpr (!Q8) {
-        if (W == 4 && a.y_f32)
-            store_f32<W, V, EXACT>(out<float>(a.y) + t * a.H, r, h);
-        else
-            store_row<XT, W, V, EXACT>(out<XT>(a.y) + t * a.H, r, h);
+        if (W == 4 && a.y_f32) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) store_values<float, W, END>(out<float>(a.y) + t * a.H, r, r.piece(u), h[u]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u) store_values<XT, W, END>(out<XT>(a.y) + t * a.H, r, r.piece(u), h[u]);
+        }
     } else {
-        const float qmax = a.q_dtype == GN_Q_INT8 ? 127.0f : 448.0f;
+        const int32_t share = lanes_of_scale(a, r);
         uint32_t m[V];
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
-            m[u] = 0;
-#pragma unroll
-            for (int e = 0; e < W; ++e) m[u] = MaxBitsOp::f(m[u], __float_as_uint(h[u][e]) & 0x7fffffffu);
-        }
-        // Lanes that share a scale: the row's, or block / W neighbours (a row of fewer lanes
-        // than that is one run).
-        const int32_t share = a.block == 0 ? r.lanes : a.block / W < r.lanes ? a.block / W : r.lanes;
+        for (int u = 0; u < V; ++u) m[u] = piece_amax(h[u]);
         if (a.block == 0) {
 #pragma unroll
             for (int u = 1; u < V; ++u) m[0] = MaxBitsOp::f(m[0], m[u]);
-            m[0] = row_all<MaxBitsOp>(m[0], r, s_max);
-        }
+            m[0] = V > 1 || r.lanes > 64 ? row_all<MaxBitsOp, true>(m[0], r, s_max) : row_all<MaxBitsOp, false>(m[0], r, s_max);
+            const Scaled sc = scale_of(m[0], a.q_dtype);
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
-            const int32_t i = r.piece(u);
-            const uint32_t amax = a.block == 0 ? m[0] : lanes_all<MaxBitsOp>(m[u], share);
-            const Scaled sc = scale_of(amax, qmax);
-            const bool bad = amax >= 0x7f800000u;
-            float q[W];
+            for (int u = 0; u < V; ++u) store_q8<W, END>(a, r, t, r.piece(u), share, sc, h[u]);
+        } else {
 #pragma unroll
-            for (int e = 0; e < W; ++e) q[e] = bad ? 0.0f : h[u][e] * sc.inv;
-            const int n = EXACT || i < r.full ? W : i == r.full ? r.tail : 0;
-            if (n) {
-                store_q<W>(out<uint8_t>(a.y) + t * a.H + i * W, n, q, a.q_dtype);
-                if (a.block == 0 ? u == 0 && r.lane == 0 : i % share == 0)
-                    a.scale[t * a.scales + (a.block == 0 ? 0 : i / share)] = sc.scale;
-            }
+            for (int u = 0; u < V; ++u)
+                store_q8<W, END>(a, r, t, r.piece(u), share, scale_of(lanes_all<MaxBitsOp>(m[u], share), a.q_dtype), h[u]);
         }
     }
 }
@@ -200,9 +234,9 @@ template <typename XT, typename RT, int W>
 hipError_t fwd(const RmsArgs& a, bool q8, const RowPlan& p, hipStream_t st)
 {
     const dim3 grid = dim3(unsigned((a.T + p.rows - 1) / p.rows));
-    return with_row<W>(p, [&](auto v, auto exact) {
+    return with_row<W>(p, a.H, [&](auto v, auto end) {
         constexpr int V = decltype(v)::value;
-        constexpr bool E = decltype(exact)::value;
+        constexpr int E = decltype(end)::value;
         return q8 ? launch(rms_fwd_kernel<XT, RT, W, V, E, true>, grid, dim3(p.block), st, a)
                   : launch(rms_fwd_kernel<XT, RT, W, V, E, false>, grid, dim3(p.block), st, a);
     });

@@ -12,82 +12,146 @@ namespace gn {
 namespace {
 
 // Workgroup b takes the row groups b, b + parts, ... (a.rows rows at once, a.lanes lanes
-// each); the next group's vectors are loaded before this group's are used. Every lane keeps
-// its columns' sums of dy * xhat in registers over all of them; at the end the workgroup adds
-// its rows' sums in LDS and leaves one partial sum for each column in the workspace.
-template <typename DT, typename HT, bool DH, int W, int V, bool EXACT, int BLOCK>
-__global__ void __launch_bounds__(BLOCK)
+// each; MANY: more than 64). DEPTH groups' loads are in flight behind the one in use, refilled
+// as soon as a group is widened. With 8 columns a lane two, so that no wait for loads is also
+// one for the stores just issued (43690 x 768 bf16: 54 us with one, 50 with two); with 16 one
+// (8192 x 4096 bf16: 48 us with one, 49 with two); fewer where registers end. Every lane keeps its columns' sums of
+// dy * xhat in registers over all groups; at the end the workgroup adds its rows' sums in LDS
+// and leaves one partial sum for each column in the workspace.
+// NT: nontemporal loads, a variant of its own, since a choice in the loop is a branch that
+// loads in flight are waited for at (8192 x 4096 bf16: 50 -> 58 us).
+// LEAN (rows of more than 512 lanes, which leave 128 registers): rows are kept as loaded and
+// widened twice, the weight and dh are read where they are used.
+template <typename DT, typename HT, bool DH, int W, int V, bool MANY, int END, int DEPTH, bool LEAN, bool NT>
+__global__ void __launch_bounds__(LEAN ? kRowMaxBlock : kBwdBlock)
 rms_bwd_kernel(RmsBwdArgs a)
 {
-    __shared__ uint32_t s_sum[2][BLOCK / 64];
-    __shared__ __align__(16) float s_dw[BLOCK * W];
+    constexpr int kBlock = LEAN ? kRowMaxBlock : kBwdBlock;
+    __shared__ uint32_t s_sum[2][kBlock / 64];
+    __shared__ __align__(16) float s_dw[kBlock * W];
     const int32_t sub = int32_t(threadIdx.x) / a.lanes;
     const Row<W> r = row_of<W>(a.H, a.lanes, int32_t(threadIdx.x) - sub * a.lanes);
-    float w[V][W], dw[V][W];
-    load_weight<W, V, EXACT>(a.w, a.w_dtype, r, w);
+    float w[LEAN ? 1 : V][W], dw[V][W];
 #pragma unroll
-    for (int u = 0; u < V; ++u)
+    for (int u = 0; u < V; ++u) {
+        if constexpr (!LEAN) load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[u]);
 #pragma unroll
         for (int e = 0; e < W; ++e) dw[u][e] = 0.0f;
-    Piece<DT, W> next_dy[V];
-    Piece<HT, W> next_h[V], next_dh[V];
-    float next_rstd;
-    const auto load = [&](int64_t t) {  // past the last row: the last row again, unused
-        t = t < a.T ? t : a.T - 1;
-        load_row<DT, W, V, EXACT>(in<DT>(a.dy) + t * a.H, r, a.nt, next_dy);
-        load_row<HT, W, V, EXACT>(in<HT>(a.h) + t * a.h_stride, r, a.nt, next_h);
-        if constexpr (DH) load_row<HT, W, V, EXACT>(in<HT>(a.dh) + t * a.H, r, a.nt, next_dh);
-        next_rstd = a.rstd[t];
+    }
+    struct Loaded {
+        Piece<DT, W> dy[V];
+        Piece<HT, W> h[V];
+        Piece<HT, W> dh[DH && !LEAN ? V : 1];
+        float rstd;
+    };
+    // The row in use and the row loaded next, with their first elements' places.
+    const int64_t step = a.parts * a.rows;
+    int64_t t = int64_t(blockIdx.x) * a.rows + sub, at = t * a.H;
+    int64_t load_t = t, load_at = at, load_h = t * a.h_stride;
+    const auto load = [&](Loaded& l) {
+        const bool past = load_t >= a.T;  // past the last row: the last row again, unused
+        const int64_t k = past ? (a.T - 1) * a.H : load_at, kh = past ? (a.T - 1) * a.h_stride : load_h;
+        load_row_as<DT, W, V, END, NT>(in<DT>(a.dy) + k, r, l.dy);
+        load_row_as<HT, W, V, END, NT>(in<HT>(a.h) + kh, r, l.h);
+        if constexpr (DH && !LEAN) load_row_as<HT, W, V, END, NT>(in<HT>(a.dh) + k, r, l.dh);
+        l.rstd = a.rstd[past ? a.T - 1 : load_t];
+        load_t += step;
+        load_at += step * a.H;
+        load_h += step * a.h_stride;
+    };
+    int phase = 0;
+    const auto group = [&](Loaded& l) {
+        if constexpr (DEPTH == 0) load(l);
+        float dy[V][W], h[V][W], d[DH && !LEAN ? V : 1][W];
+        const float rstd = l.rstd;
+        if constexpr (!LEAN) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                widen_piece<DT, W, END>(l.dy[u], r, r.piece(u), dy[u]);
+                widen_piece<HT, W, END>(l.h[u], r, r.piece(u), h[u]);
+                if constexpr (DH) l.dh[u].widen(d[u]);
+            }
+            if constexpr (DEPTH > 0) load(l);
+        }
+        float c = 0.0f;
+        if (t < a.T) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                if constexpr (LEAN) {
+                    widen_piece<DT, W, END>(l.dy[u], r, r.piece(u), dy[u]);
+                    widen_piece<HT, W, END>(l.h[u], r, r.piece(u), h[u]);
+                    load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[0]);
+                }
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    h[u][e] = h[u][e] * rstd;
+                    dw[u][e] = fmaf(dy[u][e], h[u][e], dw[u][e]);
+                    dy[u][e] = dy[u][e] * w[LEAN ? 0 : u][e];
+                }
+                c = c + tree_sumprod(dy[u], h[u]);
+            }
+        }
+        if (a.d || a.dx) {
+            c = row_sum<MANY>(c, r, s_sum[phase] + sub * (r.lanes >> 6)) * a.inv_H;
+            phase ^= 1;
+            if (t < a.T) {  // after the row's barrier
+                c = c * rstd;
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    const int32_t i = r.piece(u);
+                    if constexpr (LEAN) {
+                        l.dy[u].forget();
+                        l.h[u].forget();
+                        widen_piece<DT, W, END>(l.dy[u], r, i, dy[u]);
+                        widen_piece<HT, W, END>(l.h[u], r, i, h[u]);
+                        load_weight<W, END>(a.w, a.w_dtype, r, i, w[0]);
+                        if constexpr (DH) {
+                            load_piece<HT, W, END, false>(in<HT>(a.dh) + at, r, i, l.dh[0]);
+                            l.dh[0].widen(d[0]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < W; ++e) {
+                            h[u][e] = h[u][e] * rstd;
+                            dy[u][e] = dy[u][e] * w[0][e];
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        dy[u][e] = DH ? fmaf(dy[u][e], rstd, fmaf(-h[u][e], c, d[LEAN ? 0 : u][e]))
+                                      : fmaf(dy[u][e], rstd, -h[u][e] * c);
+                    if (a.d) store_values<HT, W, END>(out<HT>(a.d) + at, r, i, dy[u]);
+                    if (!a.dx) continue;
+                    if (sizeof(HT) == 2)  // x's type is h's, unless that is fp32
+                        store_values<HT, W, END>(out<HT>(a.dx) + at, r, i, dy[u]);
+                    else if (a.x_dtype == GN_F32)
+                        store_values<float, W, END>(out<float>(a.dx) + at, r, i, dy[u]);
+                    else if (a.x_dtype == GN_BF16)
+                        store_values<uint16_t, W, END>(out<uint16_t>(a.dx) + at, r, i, dy[u]);
+                    else
+                        store_values<_Float16, W, END>(out<_Float16>(a.dx) + at, r, i, dy[u]);
+                }
+            }
+        }
+        t += step;
+        at += step * a.H;
     };
     const int64_t groups = (a.T + a.rows - 1) / a.rows;
-    int phase = 0;
-    load(int64_t(blockIdx.x) * a.rows + sub);
-    for (int64_t g = blockIdx.x; g < groups; g += a.parts, phase ^= 1) {
-        const int64_t t = g * a.rows + sub;
-        float dy[V][W], h[V][W], d[V][W];
-        widen_row<DT, W, V>(next_dy, dy);
-        widen_row<HT, W, V>(next_h, h);
-        if constexpr (DH) widen_row<HT, W, V>(next_dh, d);
-        const float rstd = next_rstd;
-        if (g + a.parts < groups) load(t + a.parts * a.rows);
-        const bool row = t < a.T;
-        float c = 0.0f;
+    Loaded l[DEPTH > 1 ? DEPTH : 1];
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
+    for (int k = 0; k < DEPTH; ++k) load(l[k]);
+    for (int64_t g = blockIdx.x; g < groups;) {
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                h[u][e] = h[u][e] * rstd;
-                if (row) dw[u][e] = fmaf(dy[u][e], h[u][e], dw[u][e]);
-                dy[u][e] = dy[u][e] * w[u][e];
-            }
-            c = c + tree_sumprod(dy[u], h[u]);
-        }
-        if (!a.dx && !a.dres) continue;
-        c = row_sum(c, r, s_sum[phase] + sub * (r.lanes >> 6)) / float(a.H);
-        if (!row) continue;  // after the row's barrier
-#pragma unroll
-        for (int u = 0; u < V; ++u)
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-                const float v = rstd * fmaf(-h[u][e], c, dy[u][e]);
-                dy[u][e] = DH ? v + d[u][e] : v;
-            }
-        if (a.dres) store_row<HT, W, V, EXACT>(out<HT>(a.dres) + t * a.H, r, dy);
-        if (a.dx) {
-            if (sizeof(HT) == 2)
-                store_row<HT, W, V, EXACT>(out<HT>(a.dx) + t * a.H, r, dy);
-            else if (a.x_dtype == GN_F32)
-                store_f32<W, V, EXACT>(out<float>(a.dx) + t * a.H, r, dy);
-            else if (a.x_dtype == GN_BF16)
-                store_row<uint16_t, W, V, EXACT>(out<uint16_t>(a.dx) + t * a.H, r, dy);
-            else
-                store_row<_Float16, W, V, EXACT>(out<_Float16>(a.dx) + t * a.H, r, dy);
+        for (int k = 0; k < (DEPTH > 1 ? DEPTH : 1); ++k) {
+            if (k && g >= groups) break;
+            group(l[k]);
+            g += a.parts;
         }
     }
     if (!a.part) return;
     float* part = a.part + int64_t(blockIdx.x) * a.H;
     if (a.rows == 1) {
-        store_f32<W, V, EXACT>(part, r, dw);
+#pragma unroll
+        for (int u = 0; u < V; ++u) store_values<float, W, END>(part, r, r.piece(u), dw[u]);
         return;
     }
 #pragma unroll
@@ -97,10 +161,12 @@ rms_bwd_kernel(RmsBwdArgs a)
         for (int e = 0; e < W; ++e) s_dw[threadIdx.x * W + e] = dw[u][e];
         __syncthreads();
         const int32_t first = u * a.lanes * W, n = a.lanes * W;
-        for (int32_t c = threadIdx.x; c < n && first + c < a.H; c += blockDim.x) {
-            float s = s_dw[c];
-            for (int32_t k = 1; k < a.rows; ++k) s = s + s_dw[k * n + c];
-            part[first + c] = s;
+        for (int32_t k = threadIdx.x; k < n; k += blockDim.x) {
+            const int32_t i = first / W + k / W, e = k % W;
+            if (END == kTiny ? first + k >= r.H : e < r.skip(i)) continue;
+            float s = s_dw[k];
+            for (int32_t j = 1; j < a.rows; ++j) s = s + s_dw[j * n + k];
+            part[r.column(i) + e] = s;
         }
     }
 }
@@ -166,18 +232,32 @@ template <typename DT, typename HT>
 hipError_t bwd(const RmsBwdArgs& a, const BwdPlan& p, hipStream_t st)
 {
     constexpr int W = sizeof(DT) == 4 || sizeof(HT) == 4 ? 4 : 8;
-    return with_row<W>(p, [&](auto v, auto exact) {
+    return with_row<W>(p, a.H, [&](auto v, auto end) {
         constexpr int V = decltype(v)::value;
-        constexpr bool E = decltype(exact)::value;
-        const dim3 grid = dim3(unsigned(a.parts)), block = dim3(p.block);
-        // only the widest rows take more than 512 lanes, with the most pieces a lane
-        if (V * W < 32 || p.block <= kBwdBlock)
-            return a.dh ? launch(rms_bwd_kernel<DT, HT, true, W, V, E, kBwdBlock>, grid, block, st, a)
-                        : launch(rms_bwd_kernel<DT, HT, false, W, V, E, kBwdBlock>, grid, block, st, a);
+        constexpr int E = decltype(end)::value;
+        constexpr int kDepth = V * W <= 8 ? 2 : V * W <= 16 || W == 8 ? 1 : 0;
+        const auto go = [&](auto many, auto lean, auto nt) {
+            constexpr bool kMany = decltype(many)::value, kLean = decltype(lean)::value, kNt = decltype(nt)::value;
+            const dim3 grid = dim3(unsigned(a.parts)), block = dim3(p.block);
+            return a.dh ? launch(rms_bwd_kernel<DT, HT, true, W, V, kMany, E, kLean ? 0 : kDepth, kLean, kNt>, grid, block, st, a)
+                        : launch(rms_bwd_kernel<DT, HT, false, W, V, kMany, E, kLean ? 0 : kDepth, kLean, kNt>, grid, block, st, a);
+        };
+        const std::true_type yes;
+        const std::false_type no;
         if constexpr (V * W == 32)
-            return a.dh ? launch(rms_bwd_kernel<DT, HT, true, W, V, E, kRowMaxBlock>, grid, block, st, a)
-                        : launch(rms_bwd_kernel<DT, HT, false, W, V, E, kRowMaxBlock>, grid, block, st, a);
-        return hipErrorInvalidValue;
+            if (p.block > kBwdBlock) return go(yes, yes, no);
+        if constexpr (V == 1)
+            if (p.lanes <= 64) {
+                if constexpr (E == kExact)
+                    if (a.nt) return go(no, no, yes);
+                return go(no, no, no);
+            }
+        if constexpr (E == kExact)
+            if (a.nt) return go(yes, no, yes);
+        if constexpr (E == kTiny)
+            return hipErrorInvalidValue;  // one lane, above
+        else
+            return go(yes, no, no);
     });
 }
 
