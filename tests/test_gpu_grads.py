@@ -28,6 +28,11 @@ def bits(t):
     return t.view(torch.int16 if t.element_size() == 2 else torch.int32)
 
 
+# Squares of fp32 values are exact in fp64 and their sum is off by 2^-53 for each addition,
+# which is nothing beside the norm's one rounding to fp32.
+NORM = 1.01 * R.U
+
+
 def norm64(ts, kind=2.0):
     if kind == INF:
         return max([float(t.double().abs().max()) for t in ts if t.numel()], default=0.0)
@@ -54,7 +59,7 @@ def test_norm_and_clip(name, dtypes, kind):
     want = norm64(ts, kind)
     norm = gn.gn_grad_norm(ts, kind)
     assert norm.shape == () and norm.dtype == F32
-    assert abs(float(norm) - want) <= want * R.U * 1.01
+    assert abs(float(norm) - want) <= want * NORM
     for factor in (0.37, 4.0):
         limit = want * factor
         coef = min(1.0, limit / (want + 1e-6))
@@ -65,7 +70,7 @@ def test_norm_and_clip(name, dtypes, kind):
         for t, k, o in zip(ts, kept, outs):
             assert torch.equal(bits(t), bits(k)), "an input was written"
             ref = k.double() * coef
-            R.close("out", o, ref, ref.abs() * 4 * R.U + R.half_step(ref, o.dtype) * (1 + 4 * R.U))
+            R.close("out", o, ref, ref.abs() * 5 * R.U + R.half_step(ref, o.dtype) * (1 + 5 * R.U))
         n3 = gn.gn_grad_clip(ts, limit, kind)
         assert torch.equal(n3, norm)
         for t, k, o in zip(ts, kept, outs):
@@ -84,9 +89,9 @@ def test_unaligned_views_and_guards():
         say(f"views one element off alignment, {dt} to {odt}")
         n = gn.gn_grad_clip(ts, 1.0, out=outs)
         want = norm64(ts)
-        assert abs(float(n) - want) <= want * 1.01 * R.U
+        assert abs(float(n) - want) <= want * NORM
         ref = flat[1:].double() / (want + 1e-6)
-        R.close("out", dst[1:-2], ref, ref.abs() * 4 * R.U + R.half_step(ref, odt) * (1 + 4 * R.U))
+        R.close("out", dst[1:-2], ref, ref.abs() * 5 * R.U + R.half_step(ref, odt) * (1 + 5 * R.U))
         assert float(dst[0]) == 7 and bool((dst[-2:].float() == 7).all())
 
 
@@ -95,10 +100,23 @@ def test_range_of_the_norm():
     for v in (1e30, 1e-30):
         t = [torch.full((1000,), v, device="cuda"), torch.full((10,), v, device="cuda", dtype=BF)]
         want = norm64(t)
-        assert abs(float(gn.gn_grad_norm(t)) - want) <= want * 1.01 * R.U
+        assert abs(float(gn.gn_grad_norm(t)) - want) <= want * NORM
     big = [torch.full((4,), 3e38, device="cuda")]
     n = gn.gn_grad_clip(big, 1.0)
     assert math.isinf(float(n)) and bool((big[0] > 0.49).all()) and bool((big[0] < 0.51).all())   # only fp32 norm[0] overflows
+
+
+def test_a_tensor_of_several_entries():
+    n = (1 << 27) + 8197                     # longer than one entry of the table
+    say(f"{n} fp16 elements")
+    t = torch.full((n,), 0.5, dtype=F16, device="cuda")
+    t[-1], t[1 << 27] = 3.0, -2.0
+    want = math.sqrt(0.25 * (n - 2) + 13.0)
+    out = [torch.full((n,), 7.0, device="cuda")]
+    norm = gn.gn_grad_clip([t], 1.0, out=out)
+    assert abs(float(norm) - want) <= want * NORM
+    R.close("out", out[0], t.double() / (want + 1e-6), (t.double() / want).abs() * 5 * R.U)
+    assert float(gn.gn_grad_norm([t], INF)) == 3.0
 
 
 @pytest.mark.parametrize("kind", [2.0, INF], ids=["2", "inf"])
@@ -177,10 +195,10 @@ def test_a_training_step():
     want = norm64([p.grad for p in own])
     before = [p.grad.clone() for p in own]
     n = gn.clip_grad_norm_(iter(own + own[:1] + [torch.nn.Parameter(torch.ones(2, device="cuda"))]), want / 2)
-    assert abs(float(n) - want) <= want * 1.01 * R.U
+    assert abs(float(n) - want) <= want * NORM
     c = want / 2 / (want + 1e-6)
     for p, b in zip(own, before):
-        R.close("clipped", p.grad, b.double() * c, b.double().abs() * 4 * R.U + 1e-44)
+        R.close("clipped", p.grad, b.double() * c, b.double().abs() * 5 * R.U + 1e-44)
     assert abs(norm64([p.grad for p in own]) - want / 2) <= want * 1e-5
 
 

@@ -8,6 +8,7 @@ import torch
 
 import unet_groupnorm_amd as gn
 from tests import ops_reference as R
+from unet_groupnorm_amd._lib import GnGradTensor, lib
 from unet_groupnorm_amd.gn import GnError
 
 pytestmark = pytest.mark.gpu
@@ -279,6 +280,35 @@ def test_backward_of_no_rows_and_of_special_values():
     R.close("dweight", dw[cols], rdw[cols], dw_bound[cols])
 
 
+def test_offsets_past_32_bits():
+    T, H = 70001, 32760                      # 2.3e9 elements, 4.6 GB a tensor
+    say(f"{T} x {H} bf16")
+    x = torch.empty(T, H, dtype=BF, device="cuda")
+    part = rand((1000, H), BF, 91)
+    for k in range(0, T, 1000):
+        x[k:k + 1000] = part[:min(1000, T - k)]
+    w = rand((H,), BF, 92, 0.2, 1.0)
+    want, _, want_rstd = gn.gn_rms_forward(part, w)
+    y, _, rstd = gn.gn_rms_forward(x, w)
+    for k in (0, 65000, 66000, 70000):       # rows before and behind 2^31 elements (row 65552)
+        n = min(1000, T - k)
+        assert torch.equal(bits(y[k:k + n]), bits(want[:n])) and torch.equal(rstd[k:k + n], want_rstd[:n])
+    y.fill_(7)
+    gn.gn_rms_backward(x, x, rstd, w, dx=y, need_dweight=False)
+    ref = gn.gn_rms_backward(part, part, want_rstd, w, need_dweight=False)[0]
+    for k in (0, 65000, 66000, 70000):
+        n = min(1000, T - k)
+        assert torch.equal(bits(y[k:k + n]), bits(ref[:n]))
+    del y
+    q, scale, _, _ = gn.gn_rms_forward_q8(x, w, block=128)
+    qr, sr, _, _ = gn.gn_rms_forward_q8(part, w, block=128)
+    v = gn.gn_q8_dequantize(q, scale, BF, block=128)
+    vr = gn.gn_q8_dequantize(qr, sr, BF, block=128)
+    for k in (0, 65000, 66000, 70000):
+        n = min(1000, T - k)
+        assert torch.equal(q[k:k + n], qr[:n]) and torch.equal(bits(v[k:k + n]), bits(vr[:n]))
+
+
 # ------------------------------------------------------------------ autograd
 
 @pytest.mark.parametrize("x_dt,r_dt", [(F32, F32), (F32, None), (BF, BF), (F16, F32)])
@@ -348,6 +378,41 @@ def test_autograd_partial_uses():
         y = gn.rms_norm(x, w)
         (g,) = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
         g.float().sum().backward()
+
+
+def test_c_abi_refuses_memory_of_the_host():
+    T, H = 4, 64
+    x, res, y, h = (rand((T, H), BF, 93 + i) for i in range(4))
+    w, rstd, dw = rand((H,), F32, 97), rand((T,), F32, 98).abs(), rand((H,), F32, 99)
+    ws = torch.empty(lib.gn_rms_workspace_bytes(T, H), dtype=torch.uint8, device="cuda")
+    pinned = torch.zeros(1 << 14, pin_memory=True)
+    host = torch.zeros(1 << 14)
+
+    def fwd(**kw):
+        a = dict(x=x, res=res, w=w, y=y, h=h, rstd=rstd)
+        a.update(kw)
+        a = {k: v.data_ptr() for k, v in a.items()}
+        return lib.gn_rms_forward(a["x"], 1, H, a["res"], 1, a["w"], 0, T, H, 1e-6, a["y"], 1, a["h"], a["rstd"], None)
+
+    def bwd(**kw):
+        a = dict(dy=x, h=res, rstd=rstd, w=w, dh=y, dx=h, dw=dw, ws=ws)
+        a.update(kw)
+        a = {k: v.data_ptr() for k, v in a.items()}
+        return lib.gn_rms_backward(a["dy"], 1, a["h"], 1, H, a["rstd"], a["w"], 0, a["dh"], T, H, a["dx"], 1, None, a["dw"],
+                                   a["ws"], ws.numel(), None)
+
+    def norm(data, out):
+        t = (GnGradTensor * 1)()
+        t[0].data, t[0].out, t[0].numel, t[0].dtype, t[0].out_dtype = data.data_ptr(), out.data_ptr(), 64, 0, 0
+        return lib.gn_grad_clip(t, 1, 0, 1.0, rstd.data_ptr(), ws.data_ptr(), ws.numel(), None)
+
+    for call, names in ((fwd, ("x", "res", "w", "y", "h", "rstd")), (bwd, ("dy", "h", "rstd", "w", "dh", "dx", "dw", "ws"))):
+        assert call() == 0
+        for name in names:
+            for bad in (pinned, host):
+                assert call(**{name: bad}) == 8, name
+    assert norm(w, dw) == 0 and norm(pinned, dw) == 8 and norm(w, host) == 8
+    torch.cuda.synchronize()
 
 
 def test_refusals_on_the_device():

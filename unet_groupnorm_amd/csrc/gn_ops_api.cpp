@@ -38,12 +38,15 @@ int device_of(const void* p)
 // pointer argument of another device is refused.
 class OnDeviceOf {
   public:
+    // known: the device that the caller has seen every pointer and the stream to belong to, or
+    // -1 (they are looked at here).
+    explicit OnDeviceOf(int known = -1) : known_(known) {}
     int enter(const void* p, void* stream)
     {
-        const int dev = device_of(p);
+        const int dev = known_ >= 0 ? known_ : device_of(p);
         int cur = -1;
         if (dev < 0 || hipGetDevice(&cur) != hipSuccess) return GN_ERR_DEVICE;
-        if (stream) {
+        if (stream && known_ < 0) {
             hipDevice_t sdev = -1;
             if (hipStreamGetDevice(static_cast<hipStream_t>(stream), &sdev) != hipSuccess) {
                 (void)hipGetLastError();
@@ -60,6 +63,7 @@ class OnDeviceOf {
     }
     int holds(std::initializer_list<const void*> ptrs) const
     {
+        if (known_ >= 0) return GN_OK;
         for (const void* p : ptrs)
             if (p && device_of(p) != dev_) return GN_ERR_DEVICE;
         return GN_OK;
@@ -70,7 +74,7 @@ class OnDeviceOf {
     }
 
   private:
-    int prev_ = -1, dev_ = -1;
+    int known_, prev_ = -1, dev_ = -1;
 };
 
 // ------------------------------------------------------------------ row norm
@@ -117,7 +121,7 @@ void* at(void* p, int64_t bytes) { return p ? static_cast<char*>(p) + bytes : nu
 // The forward of both outputs: y is the 8-bit tensor where q_dtype >= 0.
 int forward(const void* x, int x_dtype, int64_t x_stride, const void* res, int r_dtype, const void* w, int w_dtype,
             int64_t T, int64_t H, float eps, void* y, int y_dtype, int q_dtype, int64_t block, float* scale, void* h,
-            float* rstd, void* stream)
+            float* rstd, void* stream, int device)
 {
     const bool q8 = q_dtype >= 0;
     int rc = rows_check(T, H, x_stride);
@@ -143,7 +147,7 @@ int forward(const void* x, int x_dtype, int64_t x_stride, const void* res, int r
     if ((sy.meets(sx) && !y_is_x) || meets_any(sy, {sr, sw, sh, ss, sc}) || (sh.meets(sr) && !sh.is(sr)) ||
         meets_any(sh, {sx, sw, ss, sc}) || meets_any(ss, {sx, sr, sw, sc}) || meets_any(sc, {sx, sr, sw}))
         return GN_ERR_OVERLAP;
-    OnDeviceOf dev;
+    OnDeviceOf dev(device);
     if ((rc = dev.enter(x, stream)) || (rc = dev.holds({res, w, y, h, rstd, scale}))) return rc;
     const gn::RowPlan p =
         gn::row_plan(H, x_dtype == GN_F32 || (res && r_dtype == GN_F32) || (!q8 && y_dtype == GN_F32));
@@ -289,7 +293,7 @@ int64_t partials_of(const gn_grad_tensor* t, int64_t n)
 }  // namespace
 
 int gn::grads(const gn_grad_tensor* t, int64_t n, int norm_type, bool clip, double max_norm, float* norm, void* ws,
-              size_t ws_bytes, void* stream, bool devices_known)
+              size_t ws_bytes, void* stream, int device)
 {
     int rc = tensors_check(t, n, clip);
     if (rc) return rc;
@@ -305,9 +309,9 @@ int gn::grads(const gn_grad_tensor* t, int64_t n, int norm_type, bool clip, doub
             o(clip ? t[i].out : nullptr, t[i].numel * size_of(t[i].out_dtype));
         if (t[i].numel && (meets_any(sws, {d, o}) || meets_any(sn, {d, o}))) return GN_ERR_OVERLAP;
     }
-    OnDeviceOf dev;
+    OnDeviceOf dev(device);
     if ((rc = dev.enter(norm, stream)) || (rc = dev.holds({ws}))) return rc;
-    for (int64_t i = 0; i < n && !devices_known; ++i)
+    for (int64_t i = 0; i < n && device < 0; ++i)
         if (t[i].numel && ((rc = dev.holds({t[i].data})) || (clip && t[i].out != t[i].data && (rc = dev.holds({t[i].out})))))
             return rc;
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -336,41 +340,25 @@ int gn::grads(const gn_grad_tensor* t, int64_t n, int norm_type, bool clip, doub
     });
 }
 
-extern "C" {
-
-const char* gn_ops_status_string(int status)
-{
-    switch (status) {
-        case GN_ERR_ROWS: return "invalid sizes (T >= 0, 1 <= H <= GN_RMS_MAX_COLUMNS, row stride >= H; a list of at least one tensor, sizes >= 0)";
-        case GN_ERR_OVERLAP: return "an output overlaps another argument";
-        case GN_ERR_BLOCK: return "block must be 0, 32, 64 or 128";
-        case GN_ERR_NORM: return "norm type must be GN_NORM_2 or GN_NORM_INF, and max_norm >= 0";
-        case GN_ERR_WORKSPACE: return "workspace smaller than the call's workspace query says";
-        case GN_ERR_ALIGN: return "misaligned pointer (tensors to their element, workspace to 16 bytes)";
-        case GN_ERR_DEVICE: return "a pointer argument is not device memory of the call's device, or the stream belongs to another device";
-        default: return gn_status_string(status);
-    }
-}
-
-int gn_rms_forward(const void* x, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,
-                   const void* weight, int w_dtype, int64_t T, int64_t H, float eps,
-                   void* y, int y_dtype, void* h, float* rstd, void* stream)
+int gn::rms_forward(const void* x, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,
+                    const void* weight, int w_dtype, int64_t T, int64_t H, float eps,
+                    void* y, int y_dtype, void* h, float* rstd, void* stream, int device)
 {
     return forward(x, x_dtype, x_stride, residual, r_dtype, weight, w_dtype, T, H, eps, y, y_dtype, -1, 0, nullptr, h,
-                   rstd, stream);
+                   rstd, stream, device);
 }
 
-int gn_rms_forward_q8(const void* x, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,
-                      const void* weight, int w_dtype, int64_t T, int64_t H, float eps, int64_t block,
-                      void* q, int q_dtype, float* scale, void* h, float* rstd, void* stream)
+int gn::rms_forward_q8(const void* x, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,
+                       const void* weight, int w_dtype, int64_t T, int64_t H, float eps, int64_t block,
+                       void* q, int q_dtype, float* scale, void* h, float* rstd, void* stream, int device)
 {
     if (q_dtype < 0) return GN_ERR_DTYPE;
     return forward(x, x_dtype, x_stride, residual, r_dtype, weight, w_dtype, T, H, eps, q, GN_F32, q_dtype, block,
-                   scale, h, rstd, stream);
+                   scale, h, rstd, stream, device);
 }
 
-int gn_q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, int64_t H, int64_t block,
-                     void* out, int out_dtype, void* stream)
+int gn::q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, int64_t H, int64_t block,
+                      void* out, int out_dtype, void* stream, int device)
 {
     int rc = rows_check(T, H, H);
     if (rc) return rc;
@@ -382,24 +370,16 @@ int gn_q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, 
     const int64_t scales = block ? (H + block - 1) / block : 1;
     if (meets_any(Span(out, T * H * size_of(out_dtype)), {Span(q, T * H), Span(scale, T * scales * 4)}))
         return GN_ERR_OVERLAP;
-    OnDeviceOf dev;
+    OnDeviceOf dev(device);
     if ((rc = dev.enter(q, stream)) || (rc = dev.holds({scale, out}))) return rc;
     return launch_status(gn::launch_q8_dequantize(q, q_dtype, scale, T, H, block, out, out_dtype,
                                                   static_cast<hipStream_t>(stream)));
 }
 
-size_t gn_rms_workspace_bytes(int64_t T, int64_t H)
-{
-    if (rows_check(T, H, H)) return 0;
-    // whichever the types will be
-    const int64_t parts = std::max(gn::bwd_plan(T, H, false).parts, gn::bwd_plan(T, H, true).parts);
-    return size_t(std::max<int64_t>(parts, 1)) * size_t(H) * sizeof(float);
-}
-
-int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, int64_t h_stride,
-                    const float* rstd, const void* weight, int w_dtype, const void* dh,
-                    int64_t T, int64_t H, void* dx, int x_dtype, void* dres, void* dweight,
-                    void* workspace, size_t workspace_bytes, void* stream)
+int gn::rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, int64_t h_stride,
+                     const float* rstd, const void* weight, int w_dtype, const void* dh,
+                     int64_t T, int64_t H, void* dx, int x_dtype, void* dres, void* dweight,
+                     void* workspace, size_t workspace_bytes, void* stream, int device)
 {
     int rc = rows_check(T, H, h_stride);
     if (rc) return rc;
@@ -415,7 +395,7 @@ int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, in
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (T == 0) {  // no row: the weight's gradient is zero
         if (!dweight) return GN_OK;
-        OnDeviceOf dev;
+        OnDeviceOf dev(device);
         if ((rc = dev.enter(dweight, stream)) || (rc = dev.holds({workspace}))) return rc;
         return launch_status(gn::launch_rms_dweight(static_cast<float*>(workspace), 0, H, dweight, w_dtype, st));
     }
@@ -439,7 +419,7 @@ int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, in
     if (!clear(ox, x_dtype) || !clear(orr, h_dtype) || ox.meets(orr) || meets_any(ow, {sy, sh, ss, sw, sd, sws}) ||
         meets_any(sws, {sy, sh, ss, sw, sd}))
         return GN_ERR_OVERLAP;
-    OnDeviceOf dev;
+    OnDeviceOf dev(device);
     if ((rc = dev.enter(dy, stream)) ||
         (rc = dev.holds({h, rstd, weight, dh, dx, dres, dweight, dweight ? workspace : nullptr})))
         return rc;
@@ -468,6 +448,61 @@ int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, in
     return dweight ? launch_status(gn::launch_rms_dweight(a.part, parts, H, dweight, w_dtype, st)) : GN_OK;
 }
 
+extern "C" {
+
+const char* gn_ops_status_string(int status)
+{
+    switch (status) {
+        case GN_ERR_ROWS: return "invalid sizes (T >= 0, 1 <= H <= GN_RMS_MAX_COLUMNS, row stride >= H; a list of at least one tensor, sizes >= 0)";
+        case GN_ERR_OVERLAP: return "an output overlaps another argument";
+        case GN_ERR_BLOCK: return "block must be 0, 32, 64 or 128";
+        case GN_ERR_NORM: return "norm type must be GN_NORM_2 or GN_NORM_INF, and max_norm >= 0";
+        case GN_ERR_WORKSPACE: return "workspace smaller than the call's workspace query says";
+        case GN_ERR_ALIGN: return "misaligned pointer (tensors to their element, workspace to 16 bytes)";
+        case GN_ERR_DEVICE: return "a pointer argument is not device memory of the call's device, or the stream belongs to another device";
+        default: return gn_status_string(status);
+    }
+}
+
+int gn_rms_forward(const void* x, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,
+                   const void* weight, int w_dtype, int64_t T, int64_t H, float eps,
+                   void* y, int y_dtype, void* h, float* rstd, void* stream)
+{
+    return gn::rms_forward(x, x_dtype, x_stride, residual, r_dtype, weight, w_dtype, T, H, eps, y, y_dtype, h,
+                           rstd, stream, -1);
+}
+
+int gn_rms_forward_q8(const void* x, int x_dtype, int64_t x_stride, const void* residual, int r_dtype,
+                      const void* weight, int w_dtype, int64_t T, int64_t H, float eps, int64_t block,
+                      void* q, int q_dtype, float* scale, void* h, float* rstd, void* stream)
+{
+    return gn::rms_forward_q8(x, x_dtype, x_stride, residual, r_dtype, weight, w_dtype, T, H, eps, block, q,
+                              q_dtype, scale, h, rstd, stream, -1);
+}
+
+int gn_q8_dequantize(const void* q, int q_dtype, const float* scale, int64_t T, int64_t H, int64_t block,
+                     void* out, int out_dtype, void* stream)
+{
+    return gn::q8_dequantize(q, q_dtype, scale, T, H, block, out, out_dtype, stream, -1);
+}
+
+size_t gn_rms_workspace_bytes(int64_t T, int64_t H)
+{
+    if (rows_check(T, H, H)) return 0;
+    // whichever the types will be
+    const int64_t parts = std::max(gn::bwd_plan(T, H, false).parts, gn::bwd_plan(T, H, true).parts);
+    return size_t(std::max<int64_t>(parts, 1)) * size_t(H) * sizeof(float);
+}
+
+int gn_rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, int64_t h_stride,
+                    const float* rstd, const void* weight, int w_dtype, const void* dh,
+                    int64_t T, int64_t H, void* dx, int x_dtype, void* dres, void* dweight,
+                    void* workspace, size_t workspace_bytes, void* stream)
+{
+    return gn::rms_backward(dy, dy_dtype, h, h_dtype, h_stride, rstd, weight, w_dtype, dh, T, H, dx, x_dtype, dres,
+                            dweight, workspace, workspace_bytes, stream, -1);
+}
+
 size_t gn_grad_workspace_bytes(const gn_grad_tensor* tensors, int64_t n)
 {
     return tensors_check(tensors, n, false) ? 0 : size_t(partials_of(tensors, n) + 1) * sizeof(double);
@@ -476,13 +511,13 @@ size_t gn_grad_workspace_bytes(const gn_grad_tensor* tensors, int64_t n)
 int gn_grad_norm(const gn_grad_tensor* tensors, int64_t n, int norm_type, float* norm,
                  void* workspace, size_t workspace_bytes, void* stream)
 {
-    return gn::grads(tensors, n, norm_type, false, 0.0, norm, workspace, workspace_bytes, stream, false);
+    return gn::grads(tensors, n, norm_type, false, 0.0, norm, workspace, workspace_bytes, stream, -1);
 }
 
 int gn_grad_clip(const gn_grad_tensor* tensors, int64_t n, int norm_type, double max_norm, float* norm,
                  void* workspace, size_t workspace_bytes, void* stream)
 {
-    return gn::grads(tensors, n, norm_type, true, max_norm, norm, workspace, workspace_bytes, stream, false);
+    return gn::grads(tensors, n, norm_type, true, max_norm, norm, workspace, workspace_bytes, stream, -1);
 }
 
 }  // extern "C"

@@ -3,7 +3,7 @@
 //
 // Argument marshalling only: every tensor is checked (device, dtype, sizes, layout), outputs
 // not given are allocated on the first tensor's device, that device's current HIP stream is
-// taken from torch, and the C ABI is called; its status is returned with the outputs.
+// taken from torch, and the library is called; its status is returned with the outputs.
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPStream.h>
 #include <hip/hip_runtime.h>
@@ -176,9 +176,9 @@ py::tuple rms_forward(const at::Tensor& x, const OptTensor& weight, double eps, 
     const int yc = code_of(y, "out");
     const at::Tensor h = h_of(x, residual, h_out), rstd = rstd_of(x, rstd_out, need_rstd);
     float* rp = rstd.defined() ? f32("rstd", rstd, in.r.T, in.didx) : nullptr;
-    const int status = gn_rms_forward(x.data_ptr(), in.xc, in.r.stride, in.res, in.rc, in.w, in.wc, in.r.T, in.r.H,
+    const int status = gn::rms_forward(x.data_ptr(), in.xc, in.r.stride, in.res, in.rc, in.w, in.wc, in.r.T, in.r.H,
                                       float(eps), yp, yc, residual.has_value() ? h.data_ptr() : nullptr, rp,
-                                      stream_of(in.didx));
+                                      stream_of(in.didx), in.didx);
     return py::make_tuple(y, h, or_none(rstd), status);
 }
 
@@ -197,9 +197,9 @@ py::tuple rms_forward_q8(const at::Tensor& x, const OptTensor& weight, double ep
     float* sp = f32("scale", scale, in.r.T * n, in.didx);
     const at::Tensor h = h_of(x, residual, h_out), rstd = rstd_of(x, rstd_out, need_rstd);
     float* rp = rstd.defined() ? f32("rstd", rstd, in.r.T, in.didx) : nullptr;
-    const int status = gn_rms_forward_q8(x.data_ptr(), in.xc, in.r.stride, in.res, in.rc, in.w, in.wc, in.r.T, in.r.H,
+    const int status = gn::rms_forward_q8(x.data_ptr(), in.xc, in.r.stride, in.res, in.rc, in.w, in.wc, in.r.T, in.r.H,
                                          float(eps), block, qp, qc, sp, residual.has_value() ? h.data_ptr() : nullptr,
-                                         rp, stream_of(in.didx));
+                                         rp, stream_of(in.didx), in.didx);
     return py::make_tuple(q, scale, h, or_none(rstd), status);
 }
 
@@ -213,8 +213,8 @@ py::tuple q8_dequantize(const at::Tensor& q, const at::Tensor& scale, int out_co
         out.has_value() ? *out : fresh(q.sizes(), type_of_code(out_code < 0 ? GN_F32 : out_code), q);
     void* op = like("out", o, q);
     const int oc = code_of(o, "out");
-    const int status = gn_q8_dequantize(q.data_ptr(), qc, f32("scale", scale, r.T * scales_of(r.H, block), didx), r.T,
-                                        r.H, block, op, oc, stream_of(didx));
+    const int status = gn::q8_dequantize(q.data_ptr(), qc, f32("scale", scale, r.T * scales_of(r.H, block), didx), r.T,
+                                        r.H, block, op, oc, stream_of(didx), didx);
     return py::make_tuple(o, status);
 }
 
@@ -269,9 +269,9 @@ py::tuple rms_backward(const at::Tensor& dy, const at::Tensor& h, const at::Tens
     }
     const bool apart = dres.defined() && !(dx.defined() && dres.is_same(dx));
     const int status =
-        gn_rms_backward(dyp, dyc, h.data_ptr(), hc, r.stride, rp, wp, wc, dhp, r.T, r.H,
+        gn::rms_backward(dyp, dyc, h.data_ptr(), hc, r.stride, rp, wp, wc, dhp, r.T, r.H,
                         dx.defined() ? dx.data_ptr() : nullptr, xc, apart ? dres.data_ptr() : nullptr,
-                        dw.defined() ? dw.data_ptr() : nullptr, wsp, wsb, stream_of(didx));
+                        dw.defined() ? dw.data_ptr() : nullptr, wsp, wsb, stream_of(didx), didx);
     return py::make_tuple(or_none(dx), or_none(dw), or_none(dres), status);
 }
 
@@ -318,8 +318,7 @@ py::tuple grads(const std::vector<at::Tensor>& g, const c10::optional<std::vecto
     if (ws.get_device() != didx || !ws.is_contiguous())
         throw py::value_error("workspace must be a contiguous tensor on the gradients' device");
     const size_t wsb = size_t(ws.numel()) * ws.element_size();
-    // The library still looks at norm's pointer, on whose device all tensors have been seen.
-    const int status = gn::grads(t.data(), n, norm_type, clip, max_norm, np, ws.data_ptr(), wsb, stream_of(didx), true);
+    const int status = gn::grads(t.data(), n, norm_type, clip, max_norm, np, ws.data_ptr(), wsb, stream_of(didx), didx);
     if (clip && status == GN_OK)
         for (const at::Tensor& w : out.has_value() ? *out : g)
             if (!w.is_inference()) w.unsafeGetTensorImpl()->bump_version();

@@ -28,8 +28,8 @@ struct Scaled {
 __device__ __forceinline__ Scaled scale_of(uint32_t amax, int q_dtype)
 {
     if (amax >= 0x7f800000u) return Scaled{__uint_as_float(0x7fc00000u), 0.0f};
-    const float s = fmaxf(__uint_as_float(amax) / (q_dtype == GN_Q_INT8 ? 127.0f : 448.0f), kQMin);
-    return Scaled{s, 1.0f / s};
+    const float s = fmaxf(__uint_as_float(amax) * (q_dtype == GN_Q_INT8 ? 1.0f / 127.0f : 1.0f / 448.0f), kQMin);
+    return Scaled{s, __builtin_amdgcn_rcpf(s)};  // within an ulp, and s is a normal number
 }
 
 // Bits of the largest magnitude of a piece. The comparison is that of integers, which orders

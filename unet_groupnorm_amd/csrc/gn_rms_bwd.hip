@@ -21,22 +21,29 @@ namespace {
 // NT: nontemporal loads, a variant of its own, since a choice in the loop is a branch that
 // loads in flight are waited for at (8192 x 4096 bf16: 50 -> 58 us).
 // LEAN (rows of more than 512 lanes, which leave 128 registers): rows are kept as loaded and
-// widened twice, the weight and dh are read where they are used.
+// widened twice, the weight and dh are read where they are used, and the sums of dy * xhat
+// are kept in LDS (the LDS traffic of a row is a twelfth of its time in memory).
 template <typename DT, typename HT, bool DH, int W, int V, bool MANY, int END, int DEPTH, bool LEAN, bool NT>
 __global__ void __launch_bounds__(LEAN ? kRowMaxBlock : kBwdBlock)
 rms_bwd_kernel(RmsBwdArgs a)
 {
     constexpr int kBlock = LEAN ? kRowMaxBlock : kBwdBlock;
     __shared__ uint32_t s_sum[2][kBlock / 64];
-    __shared__ __align__(16) float s_dw[kBlock * W];
+    __shared__ f32x4 s_dw[kBlock * W * (LEAN ? V : 1) / 4];
     const int32_t sub = int32_t(threadIdx.x) / a.lanes;
     const Row<W> r = row_of<W>(a.H, a.lanes, int32_t(threadIdx.x) - sub * a.lanes);
-    float w[LEAN ? 1 : V][W], dw[V][W];
+    float w[LEAN ? 1 : V][W], dw[LEAN ? 1 : V][W];
+    const auto wide_dw = [&](int u, int k) -> f32x4& { return s_dw[(u * (W / 4) + k) * kBlock + int(threadIdx.x)]; };
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-        if constexpr (!LEAN) load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[u]);
+        if constexpr (LEAN) {
 #pragma unroll
-        for (int e = 0; e < W; ++e) dw[u][e] = 0.0f;
+            for (int k = 0; k < W / 4; ++k) wide_dw(u, k) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};  // a lane's own
+        } else {
+            load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[u]);
+#pragma unroll
+            for (int e = 0; e < W; ++e) dw[u][e] = 0.0f;
+        }
     }
     struct Loaded {
         Piece<DT, W> dy[V];
@@ -81,14 +88,21 @@ rms_bwd_kernel(RmsBwdArgs a)
                     widen_piece<DT, W, END>(l.dy[u], r, r.piece(u), dy[u]);
                     widen_piece<HT, W, END>(l.h[u], r, r.piece(u), h[u]);
                     load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[0]);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) dw[0][e] = wide_dw(u, e / 4)[e & 3];
                 }
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
                     h[u][e] = h[u][e] * rstd;
-                    dw[u][e] = fmaf(dy[u][e], h[u][e], dw[u][e]);
+                    dw[LEAN ? 0 : u][e] = fmaf(dy[u][e], h[u][e], dw[LEAN ? 0 : u][e]);
                     dy[u][e] = dy[u][e] * w[LEAN ? 0 : u][e];
                 }
                 c = c + tree_sumprod(dy[u], h[u]);
+                if constexpr (LEAN) {
+#pragma unroll
+                    for (int k = 0; k < W / 4; ++k)
+                        wide_dw(u, k) = f32x4{dw[0][4 * k], dw[0][4 * k + 1], dw[0][4 * k + 2], dw[0][4 * k + 3]};
+                }
             }
         }
         if (a.d || a.dx) {
@@ -149,23 +163,30 @@ rms_bwd_kernel(RmsBwdArgs a)
     }
     if (!a.part) return;
     float* part = a.part + int64_t(blockIdx.x) * a.H;
-    if (a.rows == 1) {
+    if (LEAN || a.rows == 1) {
 #pragma unroll
-        for (int u = 0; u < V; ++u) store_values<float, W, END>(part, r, r.piece(u), dw[u]);
+        for (int u = 0; u < V; ++u) {
+            if constexpr (LEAN)
+#pragma unroll
+                for (int e = 0; e < W; ++e) dw[0][e] = wide_dw(u, e / 4)[e & 3];
+            store_values<float, W, END>(part, r, r.piece(u), dw[LEAN ? 0 : u]);
+        }
         return;
     }
+    if constexpr (LEAN) return;
+    float* sums = reinterpret_cast<float*>(s_dw);
 #pragma unroll
     for (int u = 0; u < V; ++u) {
         if (u) __syncthreads();
 #pragma unroll
-        for (int e = 0; e < W; ++e) s_dw[threadIdx.x * W + e] = dw[u][e];
+        for (int e = 0; e < W; ++e) sums[threadIdx.x * W + e] = dw[LEAN ? 0 : u][e];
         __syncthreads();
         const int32_t first = u * a.lanes * W, n = a.lanes * W;
         for (int32_t k = threadIdx.x; k < n; k += blockDim.x) {
             const int32_t i = first / W + k / W, e = k % W;
             if (END == kTiny ? first + k >= r.H : e < r.skip(i)) continue;
-            float s = s_dw[k];
-            for (int32_t j = 1; j < a.rows; ++j) s = s + s_dw[j * n + k];
+            float s = sums[k];
+            for (int32_t j = 1; j < a.rows; ++j) s = s + sums[j * n + k];
             part[r.column(i) + e] = s;
         }
     }

@@ -159,7 +159,7 @@ def clip_grad_norm_(parameters, max_norm, norm_type=2.0):
     """Clips the gradients of the parameters (a tensor or an iterable; those without a
     gradient are passed over) in place by their norm together, which is returned. A parameter
     listed twice counts once."""
-    parameters = [parameters] if isinstance(parameters, torch.Tensor) else parameters
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = list({id(p): p.grad for p in parameters if p.grad is not None}.values())
     if not grads:
         return torch.tensor(0.0)
