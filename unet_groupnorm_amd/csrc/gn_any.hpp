@@ -76,17 +76,6 @@ struct Piece {
                 w[e] = Io<_Float16>::pack(v[2 * e], v[2 * e + 1]);
         }
     }
-    // The words become unknown to the compiler, which then widens them anew instead of keeping
-    // what it widened before.
-    __device__ __forceinline__ void forget()
-    {
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-            uint32_t x = w[k];
-            asm volatile("" : "+v"(x));
-            w[k] = x;
-        }
-    }
     template <bool NT>
     __device__ __forceinline__ void store(T* p) const
     {

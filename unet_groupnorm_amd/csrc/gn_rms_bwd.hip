@@ -11,6 +11,43 @@ namespace gn {
 
 namespace {
 
+// One piece of a row: h becomes xhat, dy becomes dy * weight, dw takes dy * xhat; returns the
+// piece's sum of dy * weight * xhat.
+template <int W>
+__device__ __forceinline__ float take_sums(float (&dy)[W], float (&h)[W], const float (&w)[W], float rstd,
+                                           float (&dw)[W])
+{
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+        h[e] = h[e] * rstd;
+        dw[e] = fmaf(dy[e], h[e], dw[e]);
+        dy[e] = dy[e] * w[e];
+    }
+    return tree_sumprod(dy, h);
+}
+
+// The gradient of piece i of the row whose first element is `at`, stored: rstd * g + dh - xhat
+// * c, with g = dy * weight and c the mean of g * xhat times rstd.
+template <typename HT, bool DH, int W, int END>
+__device__ __forceinline__ void store_gradient(const RmsBwdArgs& a, const Row<W>& r, int64_t at, int32_t i,
+                                               const float (&g)[W], const float (&xhat)[W], const float (&dh)[W],
+                                               float rstd, float c)
+{
+    float d[W];
+#pragma unroll
+    for (int e = 0; e < W; ++e) d[e] = DH ? fmaf(g[e], rstd, fmaf(-xhat[e], c, dh[e])) : fmaf(g[e], rstd, -xhat[e] * c);
+    if (a.d) store_values<HT, W, END>(out<HT>(a.d) + at, r, i, d);
+    if (!a.dx) return;
+    if (sizeof(HT) == 2)  // x's type is h's, unless that is fp32
+        store_values<HT, W, END>(out<HT>(a.dx) + at, r, i, d);
+    else if (a.x_dtype == GN_F32)
+        store_values<float, W, END>(out<float>(a.dx) + at, r, i, d);
+    else if (a.x_dtype == GN_BF16)
+        store_values<uint16_t, W, END>(out<uint16_t>(a.dx) + at, r, i, d);
+    else
+        store_values<_Float16, W, END>(out<_Float16>(a.dx) + at, r, i, d);
+}
+
 // Workgroup b takes the row groups b, b + parts, ... (a.rows rows at once, a.lanes lanes
 // each; MANY: more than 64). DEPTH groups' loads are in flight behind the one in use, refilled
 // as soon as a group is widened. With 8 columns a lane two, so that no wait for loads is also
@@ -20,35 +57,25 @@ namespace {
 // and leaves one partial sum for each column in the workspace.
 // NT: nontemporal loads, a variant of its own, since a choice in the loop is a branch that
 // loads in flight are waited for at (8192 x 4096 bf16: 50 -> 58 us).
-// LEAN (rows of more than 512 lanes, which leave 128 registers): rows are kept as loaded and
-// widened twice, the weight and dh are read where they are used, and the sums of dy * xhat
-// are kept in LDS (the LDS traffic of a row is a twelfth of its time in memory).
-template <typename DT, typename HT, bool DH, int W, int V, bool MANY, int END, int DEPTH, bool LEAN, bool NT>
-__global__ void __launch_bounds__(LEAN ? kRowMaxBlock : kBwdBlock)
+template <typename DT, typename HT, bool DH, int W, int V, bool MANY, int END, int DEPTH, bool NT>
+__global__ void __launch_bounds__(kBwdBlock)
 rms_bwd_kernel(RmsBwdArgs a)
 {
-    constexpr int kBlock = LEAN ? kRowMaxBlock : kBwdBlock;
-    __shared__ uint32_t s_sum[2][kBlock / 64];
-    __shared__ f32x4 s_dw[kBlock * W * (LEAN ? V : 1) / 4];
+    __shared__ uint32_t s_sum[2][kBwdBlock / 64];
+    __shared__ __align__(16) float s_dw[kBwdBlock * W];
     const int32_t sub = int32_t(threadIdx.x) / a.lanes;
     const Row<W> r = row_of<W>(a.H, a.lanes, int32_t(threadIdx.x) - sub * a.lanes);
-    float w[LEAN ? 1 : V][W], dw[LEAN ? 1 : V][W];
-    const auto wide_dw = [&](int u, int k) -> f32x4& { return s_dw[(u * (W / 4) + k) * kBlock + int(threadIdx.x)]; };
+    float w[V][W], dw[V][W];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-        if constexpr (LEAN) {
+        load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[u]);
 #pragma unroll
-            for (int k = 0; k < W / 4; ++k) wide_dw(u, k) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};  // a lane's own
-        } else {
-            load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[u]);
-#pragma unroll
-            for (int e = 0; e < W; ++e) dw[u][e] = 0.0f;
-        }
+        for (int e = 0; e < W; ++e) dw[u][e] = 0.0f;
     }
     struct Loaded {
         Piece<DT, W> dy[V];
         Piece<HT, W> h[V];
-        Piece<HT, W> dh[DH && !LEAN ? V : 1];
+        Piece<HT, W> dh[DH ? V : 1];
         float rstd;
     };
     // The row in use and the row loaded next, with their first elements' places.
@@ -60,7 +87,7 @@ rms_bwd_kernel(RmsBwdArgs a)
         const int64_t k = past ? (a.T - 1) * a.H : load_at, kh = past ? (a.T - 1) * a.h_stride : load_h;
         load_row_as<DT, W, V, END, NT>(in<DT>(a.dy) + k, r, l.dy);
         load_row_as<HT, W, V, END, NT>(in<HT>(a.h) + kh, r, l.h);
-        if constexpr (DH && !LEAN) load_row_as<HT, W, V, END, NT>(in<HT>(a.dh) + k, r, l.dh);
+        if constexpr (DH) load_row_as<HT, W, V, END, NT>(in<HT>(a.dh) + k, r, l.dh);
         l.rstd = a.rstd[past ? a.T - 1 : load_t];
         load_t += step;
         load_at += step * a.H;
@@ -69,81 +96,27 @@ rms_bwd_kernel(RmsBwdArgs a)
     int phase = 0;
     const auto group = [&](Loaded& l) {
         if constexpr (DEPTH == 0) load(l);
-        float dy[V][W], h[V][W], d[DH && !LEAN ? V : 1][W];
+        float dy[V][W], h[V][W], d[DH ? V : 1][W];
         const float rstd = l.rstd;
-        if constexpr (!LEAN) {
 #pragma unroll
-            for (int u = 0; u < V; ++u) {
-                widen_piece<DT, W, END>(l.dy[u], r, r.piece(u), dy[u]);
-                widen_piece<HT, W, END>(l.h[u], r, r.piece(u), h[u]);
-                if constexpr (DH) l.dh[u].widen(d[u]);
-            }
-            if constexpr (DEPTH > 0) load(l);
+        for (int u = 0; u < V; ++u) {
+            widen_piece<DT, W, END>(l.dy[u], r, r.piece(u), dy[u]);
+            widen_piece<HT, W, END>(l.h[u], r, r.piece(u), h[u]);
+            if constexpr (DH) l.dh[u].widen(d[u]);
         }
+        if constexpr (DEPTH > 0) load(l);
         float c = 0.0f;
         if (t < a.T) {
 #pragma unroll
-            for (int u = 0; u < V; ++u) {
-                if constexpr (LEAN) {
-                    widen_piece<DT, W, END>(l.dy[u], r, r.piece(u), dy[u]);
-                    widen_piece<HT, W, END>(l.h[u], r, r.piece(u), h[u]);
-                    load_weight<W, END>(a.w, a.w_dtype, r, r.piece(u), w[0]);
-#pragma unroll
-                    for (int e = 0; e < W; ++e) dw[0][e] = wide_dw(u, e / 4)[e & 3];
-                }
-#pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    h[u][e] = h[u][e] * rstd;
-                    dw[LEAN ? 0 : u][e] = fmaf(dy[u][e], h[u][e], dw[LEAN ? 0 : u][e]);
-                    dy[u][e] = dy[u][e] * w[LEAN ? 0 : u][e];
-                }
-                c = c + tree_sumprod(dy[u], h[u]);
-                if constexpr (LEAN) {
-#pragma unroll
-                    for (int k = 0; k < W / 4; ++k)
-                        wide_dw(u, k) = f32x4{dw[0][4 * k], dw[0][4 * k + 1], dw[0][4 * k + 2], dw[0][4 * k + 3]};
-                }
-            }
+            for (int u = 0; u < V; ++u) c = c + take_sums<W>(dy[u], h[u], w[u], rstd, dw[u]);
         }
         if (a.d || a.dx) {
             c = row_sum<MANY>(c, r, s_sum[phase] + sub * (r.lanes >> 6)) * a.inv_H;
             phase ^= 1;
             if (t < a.T) {  // after the row's barrier
-                c = c * rstd;
 #pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    const int32_t i = r.piece(u);
-                    if constexpr (LEAN) {
-                        l.dy[u].forget();
-                        l.h[u].forget();
-                        widen_piece<DT, W, END>(l.dy[u], r, i, dy[u]);
-                        widen_piece<HT, W, END>(l.h[u], r, i, h[u]);
-                        load_weight<W, END>(a.w, a.w_dtype, r, i, w[0]);
-                        if constexpr (DH) {
-                            load_piece<HT, W, END, false>(in<HT>(a.dh) + at, r, i, l.dh[0]);
-                            l.dh[0].widen(d[0]);
-                        }
-#pragma unroll
-                        for (int e = 0; e < W; ++e) {
-                            h[u][e] = h[u][e] * rstd;
-                            dy[u][e] = dy[u][e] * w[0][e];
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < W; ++e)
-                        dy[u][e] = DH ? fmaf(dy[u][e], rstd, fmaf(-h[u][e], c, d[LEAN ? 0 : u][e]))
-                                      : fmaf(dy[u][e], rstd, -h[u][e] * c);
-                    if (a.d) store_values<HT, W, END>(out<HT>(a.d) + at, r, i, dy[u]);
-                    if (!a.dx) continue;
-                    if (sizeof(HT) == 2)  // x's type is h's, unless that is fp32
-                        store_values<HT, W, END>(out<HT>(a.dx) + at, r, i, dy[u]);
-                    else if (a.x_dtype == GN_F32)
-                        store_values<float, W, END>(out<float>(a.dx) + at, r, i, dy[u]);
-                    else if (a.x_dtype == GN_BF16)
-                        store_values<uint16_t, W, END>(out<uint16_t>(a.dx) + at, r, i, dy[u]);
-                    else
-                        store_values<_Float16, W, END>(out<_Float16>(a.dx) + at, r, i, dy[u]);
-                }
+                for (int u = 0; u < V; ++u)
+                    store_gradient<HT, DH, W, END>(a, r, at, r.piece(u), dy[u], h[u], d[DH ? u : 0], rstd, c * rstd);
             }
         }
         t += step;
@@ -163,32 +136,113 @@ rms_bwd_kernel(RmsBwdArgs a)
     }
     if (!a.part) return;
     float* part = a.part + int64_t(blockIdx.x) * a.H;
-    if (LEAN || a.rows == 1) {
+    if (a.rows == 1) {
 #pragma unroll
-        for (int u = 0; u < V; ++u) {
-            if constexpr (LEAN)
-#pragma unroll
-                for (int e = 0; e < W; ++e) dw[0][e] = wide_dw(u, e / 4)[e & 3];
-            store_values<float, W, END>(part, r, r.piece(u), dw[LEAN ? 0 : u]);
-        }
+        for (int u = 0; u < V; ++u) store_values<float, W, END>(part, r, r.piece(u), dw[u]);
         return;
     }
-    if constexpr (LEAN) return;
-    float* sums = reinterpret_cast<float*>(s_dw);
 #pragma unroll
     for (int u = 0; u < V; ++u) {
         if (u) __syncthreads();
 #pragma unroll
-        for (int e = 0; e < W; ++e) sums[threadIdx.x * W + e] = dw[LEAN ? 0 : u][e];
+        for (int e = 0; e < W; ++e) s_dw[threadIdx.x * W + e] = dw[u][e];
         __syncthreads();
         const int32_t first = u * a.lanes * W, n = a.lanes * W;
         for (int32_t k = threadIdx.x; k < n; k += blockDim.x) {
             const int32_t i = first / W + k / W, e = k % W;
             if (END == kTiny ? first + k >= r.H : e < r.skip(i)) continue;
-            float s = sums[k];
-            for (int32_t j = 1; j < a.rows; ++j) s = s + sums[j * n + k];
+            float s = s_dw[k];
+            for (int32_t j = 1; j < a.rows; ++j) s = s + s_dw[j * n + k];
             part[r.column(i) + e] = s;
         }
+    }
+}
+
+// Rows of more than 512 lanes, which leave 128 registers a lane: a row is read twice, for its
+// sums and, from the caches, for its gradient, 16 columns a lane at a time, and the sums of
+// dy * xhat are kept in LDS, whose traffic is a twelfth of the row's time in memory. One row
+// in a workgroup.
+template <typename DT, typename HT, bool DH, int W, int V, int END>
+__global__ void __launch_bounds__(kRowMaxBlock)
+rms_bwd_wide_kernel(RmsBwdArgs a)
+{
+    constexpr int kAtOnce = 16 / W, kFours = W / 4;
+    static_assert(V % kAtOnce == 0, "whole turns");
+    __shared__ uint32_t s_sum[2][kRowMaxBlock / 64];
+    __shared__ f32x4 s_dw[V * kFours * kRowMaxBlock];
+    const Row<W> r = row_of<W>(a.H, a.lanes, int32_t(threadIdx.x));
+    const auto dw_of = [&](int u, int k) -> f32x4& { return s_dw[(u * kFours + k) * kRowMaxBlock + int(threadIdx.x)]; };
+#pragma unroll 1
+    for (int u = 0; u < V; ++u)
+#pragma unroll
+        for (int k = 0; k < kFours; ++k) dw_of(u, k) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};  // a lane's own
+    int phase = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += a.parts, phase ^= 1) {
+        const int64_t at = t * a.H;
+        const DT* dy_row = in<DT>(a.dy) + at;
+        const HT* h_row = in<HT>(a.h) + t * a.h_stride;
+        const float rstd = a.rstd[t];
+        float c = 0.0f;
+#pragma unroll 1
+        for (int u0 = 0; u0 < V; u0 += kAtOnce) {
+            Piece<DT, W> rdy[kAtOnce];
+            Piece<HT, W> rh[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                load_piece<DT, W, END, false>(dy_row, r, r.piece(u0 + u), rdy[u]);
+                load_piece<HT, W, END, false>(h_row, r, r.piece(u0 + u), rh[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int32_t i = r.piece(u0 + u);
+                float dy[W], h[W], w[W], dw[W];
+                load_weight<W, END>(a.w, a.w_dtype, r, i, w);
+                widen_piece<DT, W, END>(rdy[u], r, i, dy);
+                widen_piece<HT, W, END>(rh[u], r, i, h);
+#pragma unroll
+                for (int e = 0; e < W; ++e) dw[e] = dw_of(u0 + u, e / 4)[e & 3];
+                c = c + take_sums<W>(dy, h, w, rstd, dw);
+#pragma unroll
+                for (int k = 0; k < kFours; ++k)
+                    dw_of(u0 + u, k) = f32x4{dw[4 * k], dw[4 * k + 1], dw[4 * k + 2], dw[4 * k + 3]};
+            }
+        }
+        if (!a.d && !a.dx) continue;
+        c = row_sum<true>(c, r, s_sum[phase]) * a.inv_H * rstd;
+#pragma unroll 1
+        for (int u0 = 0; u0 < V; u0 += kAtOnce) {
+            Piece<DT, W> rdy[kAtOnce];
+            Piece<HT, W> rh[kAtOnce], rdh[DH ? kAtOnce : 1];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                load_piece<DT, W, END, false>(dy_row, r, r.piece(u0 + u), rdy[u]);
+                load_piece<HT, W, END, false>(h_row, r, r.piece(u0 + u), rh[u]);
+                if constexpr (DH) load_piece<HT, W, END, false>(in<HT>(a.dh) + at, r, r.piece(u0 + u), rdh[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int32_t i = r.piece(u0 + u);
+                float dy[W], h[W], d[W], w[W];
+                load_weight<W, END>(a.w, a.w_dtype, r, i, w);
+                widen_piece<DT, W, END>(rdy[u], r, i, dy);
+                widen_piece<HT, W, END>(rh[u], r, i, h);
+                if constexpr (DH) rdh[u].widen(d);
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    h[e] = h[e] * rstd;
+                    dy[e] = dy[e] * w[e];
+                }
+                store_gradient<HT, DH, W, END>(a, r, at, i, dy, h, d, rstd, c);
+            }
+        }
+    }
+    if (!a.part) return;
+#pragma unroll 1
+    for (int u = 0; u < V; ++u) {
+        float dw[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) dw[e] = dw_of(u, e / 4)[e & 3];
+        store_values<float, W, END>(a.part + int64_t(blockIdx.x) * a.H, r, r.piece(u), dw);
     }
 }
 
@@ -257,28 +311,30 @@ hipError_t bwd(const RmsBwdArgs& a, const BwdPlan& p, hipStream_t st)
         constexpr int V = decltype(v)::value;
         constexpr int E = decltype(end)::value;
         constexpr int kDepth = V * W <= 8 ? 2 : V * W <= 16 || W == 8 ? 1 : 0;
-        const auto go = [&](auto many, auto lean, auto nt) {
-            constexpr bool kMany = decltype(many)::value, kLean = decltype(lean)::value, kNt = decltype(nt)::value;
-            const dim3 grid = dim3(unsigned(a.parts)), block = dim3(p.block);
-            return a.dh ? launch(rms_bwd_kernel<DT, HT, true, W, V, kMany, E, kLean ? 0 : kDepth, kLean, kNt>, grid, block, st, a)
-                        : launch(rms_bwd_kernel<DT, HT, false, W, V, kMany, E, kLean ? 0 : kDepth, kLean, kNt>, grid, block, st, a);
+        const dim3 grid = dim3(unsigned(a.parts)), block = dim3(p.block);
+        const auto go = [&](auto many, auto nt) {
+            constexpr bool kMany = decltype(many)::value, kNt = decltype(nt)::value;
+            return a.dh ? launch(rms_bwd_kernel<DT, HT, true, W, V, kMany, E, kDepth, kNt>, grid, block, st, a)
+                        : launch(rms_bwd_kernel<DT, HT, false, W, V, kMany, E, kDepth, kNt>, grid, block, st, a);
         };
         const std::true_type yes;
         const std::false_type no;
         if constexpr (V * W == 32)
-            if (p.block > kBwdBlock) return go(yes, yes, no);
+            if (p.block > kBwdBlock)
+                return a.dh ? launch(rms_bwd_wide_kernel<DT, HT, true, W, V, E>, grid, block, st, a)
+                            : launch(rms_bwd_wide_kernel<DT, HT, false, W, V, E>, grid, block, st, a);
         if constexpr (V == 1)
             if (p.lanes <= 64) {
                 if constexpr (E == kExact)
-                    if (a.nt) return go(no, no, yes);
-                return go(no, no, no);
+                    if (a.nt) return go(no, yes);
+                return go(no, no);
             }
         if constexpr (E == kExact)
-            if (a.nt) return go(yes, no, yes);
+            if (a.nt) return go(yes, yes);
         if constexpr (E == kTiny)
             return hipErrorInvalidValue;  // one lane, above
         else
-            return go(yes, no, no);
+            return go(yes, no);
     });
 }
 
