@@ -32,8 +32,9 @@ sys.path.insert(0, ROOT)
 
 PEAK_HBM_GBPS = 8000.0  # MI355X HBM3E peak
 METRIC = "GroupNorm fwd+bwd achieved HBM GB/s (% of MI355X peak), bf16 128³/256³ C=32 G=8"
-# Every source compiled into libgn.so: a change to any of them marks committed counter
-# records stale.
+# Every source that GroupNorm's part of libgn.so is compiled from (the row norm and the
+# gradient list are sources of their own, which it includes nothing of): a change to any of
+# them marks committed counter records stale.
 KERNEL_SOURCES = ["include/gn.h", "unet_groupnorm_amd/csrc/gn_kernels.hip", "unet_groupnorm_amd/csrc/gn_kernels_cl.hip",
                   "unet_groupnorm_amd/csrc/gn_kernels_shard.hip", "unet_groupnorm_amd/csrc/gn_device.hpp",
                   "unet_groupnorm_amd/csrc/gn_plan.cpp", "unet_groupnorm_amd/csrc/gn_plan.hpp",

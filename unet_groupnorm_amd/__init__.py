@@ -34,7 +34,7 @@ from .gn import (  # noqa: F401
 )
 from .ops import (  # noqa: F401
     RmsNormFn,
-    clip_grad_norm_,
+    clip_gradients,
     gn_grad_clip,
     gn_grad_norm,
     gn_grad_workspace_bytes,

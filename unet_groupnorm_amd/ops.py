@@ -155,7 +155,7 @@ def gn_grad_clip(grads, max_norm, norm_type=2.0, *, out=None, norm=None, workspa
     return v
 
 
-def clip_grad_norm_(parameters, max_norm, norm_type=2.0):
+def clip_gradients(parameters, max_norm, norm_type=2.0):
     """Clips the gradients of the parameters (a tensor or an iterable; those without a
     gradient are passed over) in place by their norm together, which is returned. A parameter
     listed twice counts once."""
