@@ -27,7 +27,20 @@ constexpr int kRowMaxBlock = 1024;
 constexpr int kShortBlock = 256;
 static_assert(int64_t(kRowMaxBlock) * 4 * 8 == GN_RMS_MAX_COLUMNS, "widest row: 4 pieces of 8, or 8 of 4");
 
-inline RowPlan row_plan(int64_t H, bool fp32)
+// Pieces of a lane, from the pieces of the row: as few as keep the row to few waves. Measured,
+// forward bf16 of 2^25 elements with 1, 2 and 4 pieces: rows of 1024 columns 43.9, 43.1, 60.2
+// us; of 4096 42.2, 41.9, 47.6; of 8192 45.3, 43.1, 46.8; of 12288 -, 45.7, 52.2; fp32 of 2^24
+// elements with 2, 4 and 8: rows of 4096 42.4, 42.6, 45.6; of 8192 45.6, 43.6, 45.1; of 12288 -,
+// 48.3, 49.7. The backward's workgroups hold 512 lanes (many registers each), so it goes to
+// more pieces sooner.
+inline int32_t row_pieces(int64_t n, bool fp32, bool backward)
+{
+    if (n <= 256) return 1;
+    if (n <= (fp32 || backward ? 1024 : 2048)) return 2;
+    return !fp32 || n <= (backward ? 2048 : 4096) ? 4 : 8;
+}
+
+inline RowPlan row_plan(int64_t H, bool fp32, bool backward = false)
 {
     RowPlan p;
     p.width = fp32 ? 4 : 8;
@@ -39,7 +52,7 @@ inline RowPlan row_plan(int64_t H, bool fp32)
         p.block = kShortBlock;
         p.rows = kShortBlock / p.lanes;
     } else {
-        p.vecs = n <= 256 ? 1 : n <= 1024 ? 2 : n <= 2048 || !fp32 ? 4 : 8;
+        p.vecs = row_pieces(n, fp32, backward);
         p.lanes = int32_t(((n + p.vecs - 1) / p.vecs + 63) / 64 * 64);
         p.block = p.lanes;
         p.rows = 1;
@@ -48,7 +61,7 @@ inline RowPlan row_plan(int64_t H, bool fp32)
     return p;
 }
 
-// The backward's plan: the same lanes for a row, as many rows at once as a workgroup of 512
+// The backward's plan: the lanes of a row likewise, as many rows at once as a workgroup of 512
 // threads holds (fewer where T rows would not fill the chip with such workgroups), and the
 // workgroups, each taking every parts-th group of rows and leaving one partial weight
 // gradient.
@@ -62,7 +75,7 @@ constexpr int64_t kBwdParts = 256;
 inline BwdPlan bwd_plan(int64_t T, int64_t H, bool fp32)
 {
     BwdPlan p;
-    static_cast<RowPlan&>(p) = row_plan(H, fp32);
+    static_cast<RowPlan&>(p) = row_plan(H, fp32, true);
     const int32_t least = p.lanes < 64 ? 64 / p.lanes : 1;  // rows of a whole wave
     int64_t rows = kBwdBlock / p.lanes;
     while (rows > least && (T + rows - 1) / rows < kBwdParts) rows /= 2;
@@ -135,8 +148,10 @@ constexpr int kGradEntries = 160;
 constexpr int64_t kGradGrid = 2048;
 // Lists of more tiles than this are scaled by one workgroup for each step, after a kernel
 // that takes the norm and the factor from the partials; in shorter ones each of up to
-// kGradGrid workgroups does that itself.
-constexpr int64_t kGradFoldTiles = 32768;
+// kGradGrid workgroups does that itself. Measured, separate against folded: 22.6M fp32
+// gradients 51.1 and 48.7 us, 26.2M 62.4 and 64.1 (into fp32 from bf16 47.6 and 49.0), 105M
+// 206.9 and 225.1.
+constexpr int64_t kGradFoldTiles = 12288;
 
 struct GradEntry {
     const void* data;

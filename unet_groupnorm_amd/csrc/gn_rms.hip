@@ -7,9 +7,7 @@
 // registers, reduced there, and written once. Measured, bf16 with the residual, 8192 x 4096:
 // 41.7 us, 6.44 TB/s (a copy: 6.3; counted HBM bytes equal these); 4096 x 8192 to int8: 39 us,
 // 6.0 TB/s. One workgroup for each row of more than 512 columns, and no persistent ones: the
-// loads in flight are those of the other workgroups on the CU. A lane takes 2 pieces from 257
-// on, so that a row has few waves to meet and a CU many rows: with 1, 2 and 4 pieces 8192 x
-// 4096 took 43.8, 42.2 and 44.7 us. Rows of 128 columns (131072 of them, 13.4 us, 5.0 TB/s) are
+// loads in flight are those of the other workgroups on the CU. Rows of 128 columns (131072 of them, 13.4 us, 5.0 TB/s) are
 // bound by their instructions; 4 rows a lane with one load of the weight gained 8% there and
 // lost as much at 65536 rows, and was not kept. One token (1 x 4096) takes 2.2 us on the GPU,
 // an empty launch's time, and 5 us of the host.
