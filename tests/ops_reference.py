@@ -4,18 +4,17 @@ kernels are held to.
 u = 2^-24 is the unit roundoff of fp32. The bounds are first-order rounding analysis:
 
 - rstd: the squares of a row are added in a tree of depth at most D = 40 (3 levels inside a
-  vector of 8, up to 15 more additions over a lane's vectors, 6 over a wave, 16 over waves);
-  all terms are positive, so the sum is off by at most (D + 1) u of itself, the root halves
-  that, and the division by H, the addition of eps, the root and the reciprocal add 4 u at
-  most: RSTD = 26 u.
+  piece of 8 columns, up to 8 additions over a lane's pieces, 6 over a wave, 4 over waves; 40
+  leaves room for other shapes of the tree); all terms are positive, so the sum is off by at
+  most (D + 1) u of itself and the root halves that; the mean (a product with the rounded 1 / H)
+  and the addition of eps, halved, the root and the reciprocal add 4 u at most: RSTD = 26 u.
 - y: two more products: Y = RSTD + 2 u of |y|, then the rounding to the output type, half its
   eps of |y| (and half its smallest subnormal).
-- c = mean(g * xhat): terms with 3 roundings each, the tree, the division: (D + 6) u of
+- c = mean(g * xhat): terms with 3 roundings each, the tree, the mean: (D + 6) u of
   mean|g * xhat|. d = rstd * (g - xhat * c) + dh: 6 u of each part's magnitude.
-- dweight: terms with 2 roundings, added one after the other: at most
-  (T + 64) u of the sum of the magnitudes, and no more than (2000 + 64) u, since no chain of
-  additions is longer than the 1024 partial results plus the rows of one part, for T up to
-  2^20.
+- dweight: terms with 2 roundings, added one after the other: a lane's rows (every 256th group
+  of rows), up to 512 rows of a workgroup, then 2 partial sums, 3 lane exchanges and 16 waves: at
+  most (min(T, T / 256 + 514) + 24) u of the sum of the magnitudes.
 """
 import torch
 
@@ -43,7 +42,7 @@ def rms_forward(x, weight, eps, residual=None):
 
 def rms_backward(dy, h, rstd, weight, dh=None):
     """(d, dweight, bound of d in fp32, bound of dweight in fp32) in fp64."""
-    H, T = h.shape[-1], rstd.numel()
+    T = rstd.numel()
     dy, h, rs = dy.double(), h.double(), rstd.double().unsqueeze(-1)
     g = dy if weight is None else dy * weight.double()
     xhat = h * rs
@@ -56,7 +55,7 @@ def rms_backward(dy, h, rstd, weight, dh=None):
         bound = bound + 2 * U * (d.abs() + dh.double().abs())
     lead = tuple(range(dy.dim() - 1))
     dw, mag = (dy * xhat).sum(lead), (dy * xhat).abs().sum(lead)
-    return d, dw, bound, (min(T, 2000) + 64) * U * mag + 0 * H
+    return d, dw, bound, (min(T, T // 256 + 514) + 24) * U * mag
 
 
 def e4m3_step(v):

@@ -2,6 +2,7 @@
 8-bit output, backward and autograd, over widths from one column to the widest, odd and
 unaligned ones among them, every combination of types, and special values."""
 import itertools
+import random
 
 import pytest
 import torch
@@ -278,6 +279,24 @@ def test_backward_of_no_rows_and_of_special_values():
     cols = [c for c in range(96) if c not in (5, 95)]
     assert bool(torch.isnan(dw[5])) and bool(torch.isinf(dw[95]))
     R.close("dweight", dw[cols], rdw[cols], dw_bound[cols])
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_shapes_and_types(seed):
+    rng = random.Random(seed)
+    H = rng.choice([rng.randint(1, 70), rng.randint(1, 600), rng.randint(500, 5000), rng.randint(4000, 32768)])
+    T = max(1, min(rng.randint(1, 3000), 2_000_000 // H))
+    x_dt, shift = rng.choice([BF, F16, F32]), rng.randint(0, 7)
+    r_dt, w_dt, y_dt, h_dt = (rng.choice(c) for c in ((None, x_dt, F32), (None, x_dt, F32), (x_dt, F32), (x_dt, F32)))
+    dy_dt, with_dh = rng.choice([x_dt, F32]), rng.random() < 0.5
+    q_dt, block = rng.choice([torch.int8, torch.float8_e4m3fn]), rng.choice([0, 32, 64, 128])
+    say(f"seed {seed}: T={T} H={H} x={x_dt} res={r_dt} w={w_dt} y={y_dt} h={h_dt} dy={dy_dt} {q_dt} {block} shift={shift}")
+    x = rand((T * H + shift,), x_dt, seed)[shift:].view(T, H)
+    res = None if r_dt is None else rand((T * H + shift,), r_dt, seed + 1, 2.0)[shift:].view(T, H)
+    w = None if w_dt is None else rand((H,), w_dt, seed + 2, 0.3, 1.0)
+    check_forward(x, w, res, y_dt, shift)
+    check_q8(x, w, res, q_dt, block, shift)
+    check_backward(T, H, h_dt, x_dt, dy_dt, w_dt, with_dh, seed, shift)
 
 
 def test_offsets_past_32_bits():

@@ -341,7 +341,8 @@ void capture_check(const std::vector<OptTensor>& leaves)
         if (!t.has_value() || !t->is_cuda() || !t->requires_grad() || !t->is_leaf()) continue;
         const auto cur = c10::hip::getCurrentHIPStream(t->get_device());
         hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-        if (hipStreamIsCapturing(cur.stream(), &st) != hipSuccess || st == hipStreamCaptureStatusNone) continue;
+        if (hipStreamIsCapturing(cur.stream(), &st) != hipSuccess) (void)hipGetLastError();
+        if (st == hipStreamCaptureStatusNone) continue;
         const auto acc = torch::autograd::impl::try_get_grad_accumulator(*t);
         if (!acc) continue;
         const auto s = acc->stream();  // its device type is torch's name for HIP, not HIP's own: compare ids
