@@ -252,7 +252,8 @@ rms_bwd_wide_kernel(RmsBwdArgs a)
 // A workgroup adds 32 columns of all parts: thread (slice, quad) takes 4 columns of the parts
 // slice, slice + 128, ... in order; the 8 slices of a wave are added by lane exchanges, the
 // waves in order. Bound by one trip to memory, not by bytes: a thread's few loads are in
-// flight together.
+// flight together. Workgroups of 256 threads, backward of 8192 x 4096 bf16 47.7 us against 47.8
+// with these, of 131072 x 128 20.2 against 20.5, but of 509 x 1001 fp32 9.35 against 9.1.
 constexpr int kDwBlock = 1024, kDwCols = 32, kDwSlices = kDwBlock / (kDwCols / 4);
 
 __global__ void __launch_bounds__(kDwBlock)
