@@ -269,3 +269,14 @@ def test_gradient_binding_refusals():
         with pytest.raises(err):
             call()
     assert float(gn.clip_gradients([torch.nn.Parameter(torch.ones(3))], 1.0)) == 0.0   # no gradient anywhere
+
+
+def test_backward_of_no_rows_without_a_weight_gradient():
+    """An empty tensor's address may be null; a call that has nothing to write succeeds."""
+    dy, h, rstd = torch.empty(0, 64, dtype=BF), torch.empty(0, 64), torch.empty(0)
+    for weight in (None, torch.ones(64)):
+        dx, dw, dres = gn.gn_rms_backward(dy, h, rstd, weight, x_dtype=BF, need_dweight=False)
+        assert dx.shape == dres.shape == (0, 64) and dw is None and (dx.dtype, dres.dtype) == (BF, F32)
+    x = torch.empty(2, 0, 64, requires_grad=True)
+    gn.rms_norm(x).sum().backward()
+    assert x.grad.shape == x.shape

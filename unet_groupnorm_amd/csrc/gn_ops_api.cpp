@@ -388,7 +388,7 @@ int gn::rms_backward(const void* dy, int dy_dtype, const void* h, int h_dtype, i
         !(w_dtype == GN_F32 || ((weight || dweight) && w_dtype == x_dtype)))
         return GN_ERR_DTYPE;
     if (!weight && w_dtype != GN_F32) return GN_ERR_DTYPE;
-    if (!dx && !dres && !dweight) return GN_ERR_NULL;
+    if (T > 0 && !dx && !dres && !dweight) return GN_ERR_NULL;
     if (dweight && (!workspace || !aligned(workspace, 16) || !aligned(dweight, size_of(w_dtype))))
         return workspace ? GN_ERR_ALIGN : GN_ERR_NULL;
     if (dweight && workspace_bytes < gn_rms_workspace_bytes(T, H)) return GN_ERR_WORKSPACE;
