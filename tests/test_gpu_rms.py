@@ -399,6 +399,24 @@ def test_autograd_partial_uses():
         g.float().sum().backward()
 
 
+def test_saved_tensors_that_a_later_call_overwrites():
+    def graph():
+        x, res, w = rand((6, 96), BF, 85).requires_grad_(), rand((6, 96), F32, 86), rand((96,), BF, 87)
+        return gn.rms_norm(x, w, residual=res), x.detach(), w
+
+    (y, h), x, w = graph()
+    gn.gn_rms_forward(x, w, residual=h.detach(), h=h.detach())            # the stream in place
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.float().sum().backward()
+    (y, h), x, w = graph()
+    gn.gn_rms_forward_q8(x, w, residual=h.detach(), h=h.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.float().sum().backward()
+    (y, h), x, w = graph()
+    gn.gn_rms_forward(x, w, residual=h.detach())                          # read, not written
+    y.float().sum().backward()
+
+
 def test_c_abi_refuses_memory_of_the_host():
     T, H = 4, 64
     x, res, y, h = (rand((T, H), BF, 93 + i) for i in range(4))

@@ -280,3 +280,26 @@ def test_backward_of_no_rows_without_a_weight_gradient():
     x = torch.empty(2, 0, 64, requires_grad=True)
     gn.rms_norm(x).sum().backward()
     assert x.grad.shape == x.shape
+
+
+def test_calls_mark_the_tensors_they_were_given_to_write():
+    """Calls of no rows succeed without a GPU, and tell autograd of their outputs like any other."""
+    def e(dt, *shape):
+        return torch.empty(*shape, dtype=dt)
+
+    def versions(call, **given):
+        call(**given)
+        return {k: v._version for k, v in given.items()}
+
+    x, w, res = e(BF, 0, 64), torch.ones(64, dtype=BF), e(F32, 0, 64)
+    assert versions(lambda **k: gn.gn_rms_forward(x, w, residual=res, **k), out=e(BF, 0, 64), h=e(F32, 0, 64),
+                    rstd=e(F32, 0)) == dict(out=1, h=1, rstd=1)
+    assert versions(lambda **k: gn.gn_rms_forward_q8(x, w, residual=res, **k), out=e(torch.int8, 0, 64),
+                    scale=e(F32, 0, 1), h=e(F32, 0, 64), rstd=e(F32, 0)) == dict(out=1, scale=1, h=1, rstd=1)
+    assert versions(lambda **k: gn.gn_q8_dequantize(e(torch.int8, 0, 64), e(F32, 0, 1), **k), out=e(F32, 0, 64)) == dict(out=1)
+    assert versions(lambda **k: gn.gn_rms_backward(x, res, e(F32, 0), w, x_dtype=BF, need_dweight=False, **k),
+                    dx=e(BF, 0, 64), dres=e(F32, 0, 64)) == dict(dx=1, dres=1)
+    gn.gn_rms_forward(x, w, residual=res)
+    assert (x._version, w._version, res._version) == (0, 0, 0)
+    with torch.inference_mode():                              # tensors without a version
+        gn.gn_rms_forward(e(BF, 0, 64), w, out=e(BF, 0, 64))

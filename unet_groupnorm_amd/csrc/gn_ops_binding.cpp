@@ -11,6 +11,7 @@
 #include <torch/extension.h>
 
 #include <cstdint>
+#include <initializer_list>
 #include <string>
 #include <utility>
 #include <vector>
@@ -115,6 +116,20 @@ at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& x
     return at::empty(sizes, x.options().dtype(type));
 }
 
+// Tells autograd that a call wrote into tensors of the caller's: a graph that has saved one of
+// them refuses its backward pass instead of using the new values.
+void mark_written(const at::Tensor& t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+void mark_written(int status, std::initializer_list<const OptTensor*> given)
+{
+    if (status != GN_OK) return;
+    for (const OptTensor* t : given)
+        if (t->has_value()) mark_written(**t);
+}
+
 py::object or_none(const at::Tensor& t) { return t.defined() ? py::cast(t) : py::none(); }
 
 // The sizes of x without its last dimension, and with n in its place where n >= 0.
@@ -179,6 +194,7 @@ py::tuple rms_forward(const at::Tensor& x, const OptTensor& weight, double eps, 
     const int status = gn::rms_forward(x.data_ptr(), in.xc, in.r.stride, in.res, in.rc, in.w, in.wc, in.r.T, in.r.H,
                                       float(eps), yp, yc, residual.has_value() ? h.data_ptr() : nullptr, rp,
                                       stream_of(in.didx), in.didx);
+    mark_written(status, {&out, &h_out, &rstd_out});
     return py::make_tuple(y, h, or_none(rstd), status);
 }
 
@@ -200,6 +216,7 @@ py::tuple rms_forward_q8(const at::Tensor& x, const OptTensor& weight, double ep
     const int status = gn::rms_forward_q8(x.data_ptr(), in.xc, in.r.stride, in.res, in.rc, in.w, in.wc, in.r.T, in.r.H,
                                          float(eps), block, qp, qc, sp, residual.has_value() ? h.data_ptr() : nullptr,
                                          rp, stream_of(in.didx), in.didx);
+    mark_written(status, {&out, &scale_out, &h_out, &rstd_out});
     return py::make_tuple(q, scale, h, or_none(rstd), status);
 }
 
@@ -215,6 +232,7 @@ py::tuple q8_dequantize(const at::Tensor& q, const at::Tensor& scale, int out_co
     const int oc = code_of(o, "out");
     const int status = gn::q8_dequantize(q.data_ptr(), qc, f32("scale", scale, r.T * scales_of(r.H, block), didx), r.T,
                                         r.H, block, op, oc, stream_of(didx), didx);
+    mark_written(status, {&out});
     return py::make_tuple(o, status);
 }
 
@@ -272,6 +290,7 @@ py::tuple rms_backward(const at::Tensor& dy, const at::Tensor& h, const at::Tens
         gn::rms_backward(dyp, dyc, h.data_ptr(), hc, r.stride, rp, wp, wc, dhp, r.T, r.H,
                         dx.defined() ? dx.data_ptr() : nullptr, xc, apart ? dres.data_ptr() : nullptr,
                         dw.defined() ? dw.data_ptr() : nullptr, wsp, wsb, stream_of(didx), didx);
+    mark_written(status, {&dx_out, &dres_out, &dweight_out});
     return py::make_tuple(or_none(dx), or_none(dw), or_none(dres), status);
 }
 
@@ -321,7 +340,8 @@ py::tuple grads(const std::vector<at::Tensor>& g, const c10::optional<std::vecto
     const int status = gn::grads(t.data(), n, norm_type, clip, max_norm, np, ws.data_ptr(), wsb, stream_of(didx), didx);
     if (clip && status == GN_OK)
         for (const at::Tensor& w : out.has_value() ? *out : g)
-            if (!w.is_inference()) w.unsafeGetTensorImpl()->bump_version();
+            mark_written(w);
+    mark_written(status, {&norm_out});
     return py::make_tuple(norm, status);
 }
 

@@ -7,7 +7,8 @@ are not given on the inputs' device, and calls the library on that device's curr
 a non-zero status becomes a GnError. All arithmetic happens in the HIP kernels.
 
 A row is the last dimension. x may be a view whose rows are evenly spaced (a slice of a wider
-projection); every other tensor is contiguous. Nothing here waits for the GPU.
+projection); every other tensor is contiguous. Nothing here waits for the GPU. Tensors that
+are given to be written count as modified in place for autograd.
 """
 import torch
 from torch.autograd.function import once_differentiable
