@@ -76,7 +76,8 @@ typedef enum gn_q8 {
  * Forward with the output in 8 bits: y as above, kept in fp32, and for each row (block == 0)
  * or each run of `block` columns (32, 64 or 128; a row's last may be shorter)
  *   scale = max(max|y| / qmax, 2^-126),  q = y / scale rounded to nearest, ties to even,
- * with qmax = 127 or 448 (scale and the quotient's divisor within 2 ulp of these in fp32). scale is [T][ceil(H / block)] fp32 ([T] for block == 0). Where a
+ * with qmax = 127 or 448. The scale is the correctly rounded fp32 quotient; y / scale is taken
+ * in fp32 to (1/2 + 2^-20) ulp. scale is [T][ceil(H / block)] fp32 ([T] for block == 0). Where a
  * run holds a NaN or an infinity its scale is NaN and its q are 0 (so q * scale is NaN).
  * q [T][H]; h, rstd and the allowed overlaps as gn_rms_forward's (q overlaps nothing).
  * One kernel.

@@ -190,6 +190,33 @@ def test_q8(q_dtype, block):
         check_q8(rand((T, H), x_dt, 20), rand((H,), x_dt if H % 2 else F32, 22, 0.3, 1.0), res, q_dtype, block, shift)
 
 
+@pytest.mark.parametrize("q_dtype", [torch.int8, torch.float8_e4m3fn], ids=["int8", "e4m3"])
+@pytest.mark.parametrize("block", [0, 32, 64, 128])
+def test_q8_bits_follow_from_the_norm(q_dtype, block):
+    """Given h, rstd and the weight, y is two rounded products, the scale one rounded quotient and
+    q another (whose fp32 value may be another neighbour only 2^-20 ulp from halfway between two;
+    none of these is): nothing is left to a tolerance, and every bit is compared. Weights down to
+    subnormal numbers, where the scale meets its floor."""
+    qmax = 127.0 if q_dtype == torch.int8 else 448.0
+    for T, H, x_dt, r_dt, size in ((400, 4096, BF, BF, 1.0), (300, 1001, F16, F32, 1.0), (900, 100, F32, None, 1.0),
+                                   (5, 3, BF, None, 1.0), (64, 8200, BF, None, 1e-28), (64, 520, F32, F32, 1e-33),
+                                   (64, 1024, BF, BF, 1e-36), (64, 520, F32, F32, 2e-37), (64, 96, F32, None, 1e-39),
+                                   (64, 4096, F16, F16, 1e-43), (16, 4096, F32, None, 1e30)):
+        say(f"q8 bits {q_dtype} block={block} T={T} H={H} {x_dt} res={r_dt} weights of {size}")
+        x, w = rand((T, H), x_dt, 23, 1.5), rand((H,), F32, 24, 0.3 * size, size)
+        res = None if r_dt is None else rand((T, H), r_dt, 25, 2.0)
+        q, scale, h, rstd = gn.gn_rms_forward_q8(x, w, EPS, residual=res, q_dtype=q_dtype, block=block, need_rstd=True)
+        y = (h.cpu().float() * rstd.cpu().unsqueeze(-1)) * w.cpu()
+        B = block or H
+        n = -(-H // B)
+        runs = torch.nn.functional.pad(y, (0, n * B - H)).view(T, n, B)
+        want = (runs.abs().amax(-1) / qmax).clamp(min=2.0 ** -126)
+        assert torch.equal(bits(scale.cpu()), bits(want)), "scale"
+        v = (runs / want.unsqueeze(-1)).view(T, n * B)[:, :H]
+        wq = torch.round(v).to(torch.int8) if q_dtype == torch.int8 else v.to(torch.float8_e4m3fn)
+        assert torch.equal(q.cpu().float(), wq.float()), "q"
+
+
 # ------------------------------------------------------------------ backward
 
 BWD_TYPES = [(h, x, dy) for h, x, dy in itertools.product((BF, F16, F32), repeat=3)
