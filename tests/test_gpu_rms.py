@@ -90,6 +90,20 @@ def test_forward_types(types):
         check_forward(rand((T, H), x_dt, 4), w, res, y_dt)
 
 
+@pytest.mark.parametrize("H", [1, 3, 41, 64, 100, 1001, 1531, 4096, 8200, 32761])
+def test_rstd_of_exact_sums(H):
+    """Rows of small integers: the sum of squares is below 2^24, so exact in any order. What is
+    left is the mean's rounding, halved by the root, and the root's own: 1.5 u."""
+    for dt in (BF, F16, F32):
+        say(f"rstd of integers, H={H} {dt}")
+        g = torch.Generator(device="cuda")
+        g.manual_seed(26)
+        x = torch.randint(1, 30, (2000, H), generator=g, device="cuda").to(dt)
+        rstd = gn.gn_rms_forward(x, None, 0.0)[2]
+        ref = 1.0 / torch.sqrt(x.double().square().mean(-1))
+        R.close("rstd", rstd, ref, ref * 1.5 * R.U * (1 + 2.0 ** -16))
+
+
 def test_forward_strided_rows_and_leading_dimensions():
     wide = rand((6, 5, 300), BF, 7)
     for x in (wide[..., 100:228], wide[..., 1:300], wide[:, :1, 3:40], rand((40,), BF, 8), rand((0, 16), BF, 9)):

@@ -120,6 +120,18 @@ __device__ __forceinline__ void store_q(uint8_t* p, int lo, int hi, float (&v)[W
 
 // ------------------------------------------------------------------ forward
 
+// 1 / sqrt(ss / H + eps) from an estimate r and v, the mean (a product with the rounded 1 / H,
+// corrected by its remainder) plus eps, each rounded once: p + lo = v * r exactly, so e = 1 - v
+// * r^2 is known to its last bits, and r + r * e / 2 is off by 3/8 e^2 of it before its one
+// rounding. An estimate of zero or infinity has no correction.
+__device__ __forceinline__ float inverse_rms(float ss, const RmsArgs& a)
+{
+    const float r = rsqrtf(fmaf(ss, a.inv_H, a.eps)), m = ss * a.inv_H;
+    const float v = fmaf(fmaf(-m, float(a.H), ss), a.inv_H, m) + a.eps;
+    const float p = v * r, lo = fmaf(v, r, -p), e = fmaf(-lo, r, fmaf(-p, r, 1.0f));
+    return r > 0.0f && r < __builtin_huge_valf() ? fmaf(0.5f * r, e, r) : r;
+}
+
 // One piece's output in 8 bits; `share` lanes share the scale, and the first of them stores it.
 template <int W, int END>
 __device__ __forceinline__ void store_q8(const RmsArgs& a, const Row<W>& r, int64_t t, int32_t i, int32_t share,
@@ -179,7 +191,7 @@ rms_fwd_kernel(RmsArgs a)
 #pragma unroll
         for (int u = 0; u < V; ++u) store_values<HT, W, END>(out<HT>(a.h) + t * a.H, r, r.piece(u), h[u]);
     }
-    const float rstd = 1.0f / sqrtf(fmaf(ss, a.inv_H, a.eps));
+    const float rstd = inverse_rms(ss, a);
     if (a.rstd && r.lane == 0) a.rstd[t] = rstd;
 #pragma unroll
     for (int u = 0; u < V; ++u)
