@@ -369,6 +369,56 @@ def test_offsets_past_32_bits():
         assert torch.equal(q[k:k + n], qr[:n]) and torch.equal(bits(v[k:k + n]), bits(vr[:n]))
 
 
+# ------------------------------------------------------------------ calls past the last-level cache
+#
+# Calls that move over 200 MiB load their rows with another cache policy, in the backward by
+# kernels of their own for rows of whole pieces: one width for each number of pieces a lane.
+
+BIG = [(8800, 4096, BF), (18000, 2048, F16), (400000, 128, BF), (100000, 512, BF), (2200, 16384, BF), (2200, 16384, F16),
+       (65536, 512, F32), (400000, 128, F32), (4500, 4096, F32), (2200, 8192, F32), (1100, 16384, F32)]
+
+
+@pytest.mark.parametrize("T,H,dt", BIG, ids=lambda v: str(v).replace("torch.", ""))
+def test_backward_past_the_cache(T, H, dt):
+    assert T * H * dt.itemsize * 3 > 200 << 20
+    say(f"backward T={T} H={H} {dt} with and without dh")
+    check_backward(T, H, dt, dt, dt, dt, True, 100)
+    check_backward(T, H, dt, dt, dt, None, False, 104)
+    if dt != F32:
+        say(f"backward T={T} H={H} {dt} of an fp32 stream")
+        check_backward(T, H, F32, dt, dt, F32, True, 108)
+        check_backward(T, H, dt, dt, F32, F32, True, 112)
+
+
+@pytest.mark.parametrize("T,H", [(8192, 4096), (400000, 128), (2200, 16384), (40000, 1001)])
+def test_backward_past_the_cache_in_place(T, H):
+    say(f"backward in place T={T} H={H}")
+    dy, h, dh = rand((T, H), BF, 120), rand((T, H), BF, 121), rand((T, H), BF, 122)
+    w = rand((H,), BF, 123, 0.2, 1.0)
+    rstd = gn.gn_rms_forward(h, w, EPS)[2]
+    dx, dw, _ = gn.gn_rms_backward(dy, h, rstd, w, dh=dh)
+    for place in ("dy", "h", "dh"):
+        t = {"dy": dy.clone(), "h": h.clone(), "dh": dh.clone()}
+        dw2 = gn.gn_rms_backward(t["dy"], t["h"], rstd, w, dh=t["dh"], dx=t[place])[1]
+        assert torch.equal(bits(dx), bits(t[place])) and torch.equal(bits(dw), bits(dw2)), place
+
+
+@pytest.mark.parametrize("T,H,x_dt,r_dt", [(16384, 2048, BF, BF), (400000, 128, F16, F16), (400000, 128, BF, F32),
+                                           (3000, 16384, BF, BF), (40000, 1001, BF, BF), (9000, 4096, F32, F32),
+                                           (10000, 4096, F16, F32), (400000, 192, BF, None)])
+def test_forward_and_q8_past_the_cache(T, H, x_dt, r_dt):
+    say(f"forward and q8 T={T} H={H} {x_dt} res={r_dt}")
+    x, w = rand((T, H), x_dt, 130, 1.5), rand((H,), F32, 131, 0.2, 1.0)
+    res = None if r_dt is None else rand((T, H), r_dt, 132, 2.0)
+    check_forward(x, w, res, x_dt)
+    check_q8(x, w, res, torch.int8, 0)
+    check_q8(x, w, res, torch.float8_e4m3fn, 32)
+    y, h, rstd = gn.gn_rms_forward(x, w, EPS, residual=res)
+    h = h.clone()
+    gn.gn_rms_forward(x, w, EPS, residual=res, out=x, h=res)
+    assert torch.equal(bits(x), bits(y)) and (res is None or torch.equal(bits(res), bits(h)))
+
+
 # ------------------------------------------------------------------ autograd
 
 @pytest.mark.parametrize("x_dt,r_dt", [(F32, F32), (F32, None), (BF, BF), (F16, F32)])
