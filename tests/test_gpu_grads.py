@@ -81,6 +81,53 @@ def test_norm_and_clip(name, dtypes, kind):
         ts = kept
 
 
+# Lists of more than 12288 tiles of 2048 elements take the factor from a kernel between the two
+# passes; the first of these is the longest that does not.
+LONG = {
+    "12288 tiles": [12288 * 2048],
+    "12289 tiles": [12288 * 2048 + 1],
+    "two long tensors": [30_000_003, 64, 20_000_000],
+    "several tables": [60_000 + (i * 7919) % 70_001 for i in range(400)],
+    "biases beside one long tensor": [26_000_000] + [1 + (i * 37) % 300 for i in range(200)],
+}
+
+
+@pytest.mark.parametrize("kind", [2.0, INF], ids=["2", "inf"])
+@pytest.mark.parametrize("dtypes", [(F32,), (BF,), (F16,), (BF, F32, F16)], ids=["fp32", "bf16", "fp16", "mixed"])
+@pytest.mark.parametrize("name", list(LONG))
+def test_norm_and_clip_of_long_lists(name, dtypes, kind, monkeypatch):
+    monkeypatch.setitem(LISTS, name, LONG[name])
+    test_norm_and_clip(name, dtypes, kind)
+
+
+def test_long_unaligned_views_and_guards():
+    sizes = [3, 8193, 26_000_001, 1, 40001, 64]
+    for dt, odt in ((BF, BF), (BF, F32), (F16, F16), (F32, F32)):
+        flat, dst = rand(sum(sizes) + 1, dt, 5), torch.full((sum(sizes) + 3,), 7.0, device="cuda", dtype=odt)
+        ts, outs = list(flat[1:].split(sizes)), list(dst[1:-2].split(sizes))
+        say(f"a long list of views one element off alignment, {dt} to {odt}")
+        n = gn.gn_grad_clip(ts, 1.0, out=outs)
+        want = norm64(ts)
+        assert abs(float(n) - want) <= want * NORM
+        ref = flat[1:].double() / (want + 1e-6)
+        R.close("out", dst[1:-2], ref, ref.abs() * 5 * R.U + R.half_step(ref, odt) * (1 + 5 * R.U))
+        assert float(dst[0]) == 7 and bool((dst[-2:].float() == 7).all())
+
+
+@pytest.mark.parametrize("kind", [2.0, INF], ids=["2", "inf"])
+def test_nan_and_infinity_in_a_long_list(kind):
+    for bad in (float("nan"), INF, -INF):
+        for dt in (BF, F32):
+            t = [rand(100, BF, 1), rand(26_000_001, dt, 2)]
+            t[1][-1] = bad
+            n = gn.gn_grad_clip(t, 1.0, kind)
+            if math.isnan(bad):
+                assert math.isnan(float(n)) and bool(torch.isnan(t[0]).all()) and bool(torch.isnan(t[1]).all())
+            else:
+                assert float(n) == INF and float(t[0].abs().max()) == 0
+                assert bool(torch.isnan(t[1][-1])) and int(torch.isnan(t[1]).sum()) == 1
+
+
 def test_unaligned_views_and_guards():
     sizes = [3, 8193, 1000, 1, 40001, 64]
     for dt, odt in ((BF, BF), (BF, F32), (F16, F32), (F32, F32)):
