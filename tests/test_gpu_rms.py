@@ -303,6 +303,14 @@ def test_backward_parts_in_place_and_bits():
         assert torch.equal(bits(dx), bits(t[place])), place
 
 
+def test_backward_into_a_given_residual_gradient():
+    h, dy, rstd = rand((9, 200), BF, 140), rand((9, 200), BF, 141), rand((9,), F32, 142).abs()
+    want = gn.gn_rms_backward(dy, h, rstd, None)[0]
+    dres = torch.full_like(h, 7)
+    dx, _, got = gn.gn_rms_backward(dy, h, rstd, None, dres=dres)
+    assert got is dres and torch.equal(bits(dres), bits(want)) and torch.equal(bits(dx), bits(want))
+
+
 def test_backward_of_no_rows_and_of_special_values():
     w = rand((64,), BF, 64)
     dx, dw, _ = gn.gn_rms_backward(rand((0, 64), BF, 65), rand((0, 64), BF, 66), rand((0,), F32, 67), w)

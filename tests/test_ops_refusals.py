@@ -303,3 +303,23 @@ def test_calls_mark_the_tensors_they_were_given_to_write():
     assert (x._version, w._version, res._version) == (0, 0, 0)
     with torch.inference_mode():                              # tensors without a version
         gn.gn_rms_forward(e(BF, 0, 64), w, out=e(BF, 0, 64))
+
+
+def test_backward_writes_every_output_it_is_given():
+    """A dres given beside h of x's dtype is asked for by that; one that a flag declines is refused."""
+    def e(*shape, dt=BF):
+        return torch.empty(*shape, dtype=dt)
+
+    x, rstd, w = e(0, 64), e(0, dt=F32), torch.ones(64, dtype=BF)
+    dres = e(0, 64)
+    got = gn.gn_rms_backward(x, x, rstd, w, dres=dres, need_dweight=False)
+    assert got[2] is dres and dres._version == 1 and got[0] is not dres
+    dx, dres = e(0, 64), e(0, 64)
+    got = gn.gn_rms_backward(x, x, rstd, w, dx=dx, dres=dres, need_dweight=False)
+    assert got[0] is dx and got[2] is dres and (dx._version, dres._version) == (1, 1)
+    got = gn.gn_rms_backward(x, x, rstd, w, dres=dres, need_dx=False, need_dweight=False)
+    assert got[0] is None and got[2] is dres
+    for name, given in (("dx", e(0, 64)), ("dres", e(0, 64)), ("dweight", e(64))):
+        with pytest.raises(ValueError, match=name):
+            gn.gn_rms_backward(x, x, rstd, w, **{"need_dweight": False, name: given, "need_" + name: False})
+        assert given._version == 0

@@ -236,6 +236,12 @@ py::tuple q8_dequantize(const at::Tensor& q, const at::Tensor& scale, int out_co
     return py::make_tuple(o, status);
 }
 
+// An output that the caller gives and at the same time does not want.
+void wanted(const OptTensor& given, bool need, const std::string& name)
+{
+    if (given.has_value() && !need) throw py::value_error(name + " is given, but need_" + name + " declines it");
+}
+
 py::tuple rms_backward(const at::Tensor& dy, const at::Tensor& h, const at::Tensor& rstd, const OptTensor& weight,
                        const OptTensor& dh, int x_code, bool need_dx, bool need_dres, bool need_dweight,
                        const OptTensor& workspace, const OptTensor& dx_out, const OptTensor& dres_out,
@@ -256,6 +262,9 @@ py::tuple rms_backward(const at::Tensor& dy, const at::Tensor& h, const at::Tens
         dhp = like("dh", *dh, h);
         if (dh->scalar_type() != h.scalar_type()) throw py::type_error("dh must have h's dtype");
     }
+    wanted(dx_out, need_dx, "dx");
+    wanted(dres_out, need_dres, "dres");
+    wanted(dweight_out, need_dweight, "dweight");
     at::Tensor dx, dres, dw;
     if (need_dx) {
         dx = dx_out.has_value() ? *dx_out : fresh(h.sizes(), type_of_code(xc), h);

@@ -85,11 +85,12 @@ def gn_rms_backward(dy, h, rstd, weight, *, dh=None, x_dtype=None, need_dx=True,
     """Returns (dx, dweight, dres), each None where not needed. h and rstd are
     gn_rms_forward's; dh is the gradient that reaches h through the residual stream (None:
     none). The gradients of x and of the residual are one value, written in x_dtype (h.dtype
-    by default) as dx and in h's dtype as dres: one tensor where the dtypes agree. need_dres
-    defaults to whether they differ. dweight has weight's dtype (float32 without a weight)."""
+    by default) as dx and in h's dtype as dres: one tensor where the dtypes agree and no dres is
+    given. need_dres defaults to whether they differ or dres is given. dweight has weight's dtype
+    (float32 without a weight). A given output that its flag declines is refused."""
     code = _out_code(x_dtype)
     if need_dres is None:
-        need_dres = x_dtype is not None and x_dtype != h.dtype
+        need_dres = dres is not None or (x_dtype is not None and x_dtype != h.dtype)
     dx, dweight, dres, status = _gnbind.rms_backward(dy, h, rstd, weight, dh, code, need_dx, need_dres, need_dweight,
                                                      workspace, dx, dres, dweight)
     _check("gn_rms_backward", status)
