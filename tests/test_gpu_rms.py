@@ -498,6 +498,16 @@ def test_autograd_partial_uses():
         g.float().sum().backward()
 
 
+@pytest.mark.parametrize("shape", [(1, 64), (1, 1, 64), (64, 1)], ids=str)
+def test_autograd_of_a_weight_that_is_not_a_vector(shape):
+    x = rand((4, 5, 64), BF, 88)
+    flat = rand((64,), BF, 89).requires_grad_()
+    w = flat.detach().reshape(shape).requires_grad_()
+    for weight in (flat, w):
+        gn.rms_norm(x, weight).float().square().sum().backward()
+    assert w.grad.shape == shape and torch.equal(bits(w.grad.reshape(64)), bits(flat.grad))
+
+
 def test_saved_tensors_that_a_later_call_overwrites():
     def graph():
         x, res, w = rand((6, 96), BF, 85).requires_grad_(), rand((6, 96), F32, 86), rand((96,), BF, 87)

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import unet_groupnorm_amd as gn
+from unet_groupnorm_amd import _gnbind
 from unet_groupnorm_amd._lib import GN_BF16, GN_F16, GN_F32, OPS_STATUS_NAMES, GnGradTensor, lib
 from unet_groupnorm_amd.gn import GnError
 
@@ -323,3 +324,13 @@ def test_backward_writes_every_output_it_is_given():
         with pytest.raises(ValueError, match=name):
             gn.gn_rms_backward(x, x, rstd, w, **{"need_dweight": False, name: given, "need_" + name: False})
         assert given._version == 0
+
+
+@pytest.mark.parametrize("shape", [(64,), (1, 64), (1, 1, 64), (64, 1), (8, 8)], ids=str)
+def test_a_weights_gradient_has_the_weights_shape(shape):
+    x, rstd = _x(), torch.ones(3, 5)
+    for dt in (BF, F32):
+        dw = _gnbind.rms_backward(x, x, rstd, torch.ones(shape, dtype=dt), None, -1, True, False, True, None, None, None, None)[1]
+        assert dw.shape == shape and dw.dtype == dt
+    dw = _gnbind.rms_backward(x, x, rstd, None, None, -1, True, False, True, None, None, None, None)[1]
+    assert dw.shape == (64,) and dw.dtype == F32

@@ -279,7 +279,8 @@ py::tuple rms_backward(const at::Tensor& dy, const at::Tensor& h, const at::Tens
         if (dres.scalar_type() != h.scalar_type()) throw py::type_error("dres must have h's dtype");
     }
     if (need_dweight) {
-        dw = dweight_out.has_value() ? *dweight_out : fresh({r.H}, type_of_code(wc), h);
+        if (dweight_out.has_value()) dw = *dweight_out;
+        else dw = weight.has_value() ? fresh(weight->sizes(), type_of_code(wc), h) : fresh({r.H}, type_of_code(wc), h);
         vec("dweight", dw, r.H, didx);
         if (code_of(dw, "dweight") != wc) throw py::type_error("dweight must have weight's dtype");
     }

@@ -42,9 +42,9 @@ def gn_rms_forward(x, weight, eps=1e-6, *, residual=None, out_dtype=None, need_r
     without a residual); rstd = 1 / sqrt(mean(h^2) + eps) over each row, fp32; y = h * rstd *
     weight, computed in fp32 and rounded once to out_dtype (x.dtype by default, or float32).
 
-    residual: x's dtype or float32. weight: x's dtype or float32, None for ones. h=residual
-    updates the residual stream in place, out=x overwrites a contiguous x. rstd, which the
-    backward needs, is None with need_rstd=False."""
+    residual: x's dtype or float32. weight: x's dtype or float32, H elements in any shape, None for
+    ones. h=residual updates the residual stream in place, out=x overwrites a contiguous x. rstd,
+    which the backward needs, is None with need_rstd=False."""
     y, h, rstd, status = _gnbind.rms_forward(x, weight, eps, residual, _out_code(out_dtype), need_rstd, out, h, rstd)
     _check("gn_rms_forward", status)
     return y, h, rstd
@@ -86,8 +86,8 @@ def gn_rms_backward(dy, h, rstd, weight, *, dh=None, x_dtype=None, need_dx=True,
     gn_rms_forward's; dh is the gradient that reaches h through the residual stream (None:
     none). The gradients of x and of the residual are one value, written in x_dtype (h.dtype
     by default) as dx and in h's dtype as dres: one tensor where the dtypes agree and no dres is
-    given. need_dres defaults to whether they differ or dres is given. dweight has weight's dtype
-    (float32 without a weight). A given output that its flag declines is refused."""
+    given. need_dres defaults to whether they differ or dres is given. dweight has weight's shape
+    and dtype (H float32 elements without a weight). A given output that its flag declines is refused."""
     code = _out_code(x_dtype)
     if need_dres is None:
         need_dres = dres is not None or (x_dtype is not None and x_dtype != h.dtype)
