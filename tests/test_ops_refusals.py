@@ -334,3 +334,24 @@ def test_a_weights_gradient_has_the_weights_shape(shape):
         assert dw.shape == shape and dw.dtype == dt
     dw = _gnbind.rms_backward(x, x, rstd, None, None, -1, True, False, True, None, None, None, None)[1]
     assert dw.shape == (64,) and dw.dtype == F32
+
+
+def test_a_dtype_that_contradicts_the_given_output_is_refused():
+    def e(dt, *shape):
+        return torch.empty(*shape, dtype=dt)
+
+    E4, x, w, scale = torch.float8_e4m3fn, e(BF, 0, 64), torch.ones(64), e(F32, 0, 1)
+    with pytest.raises(TypeError, match="out_dtype"):
+        gn.gn_rms_forward(x, w, out_dtype=F32, out=e(BF, 0, 64))
+    for asked, given in ((torch.int8, E4), (E4, torch.int8)):
+        with pytest.raises(TypeError, match="q_dtype"):
+            gn.gn_rms_forward_q8(x, w, q_dtype=asked, out=e(given, 0, 64))
+    with pytest.raises(TypeError, match="out_dtype"):
+        gn.gn_q8_dequantize(e(torch.int8, 0, 64), scale, F32, out=e(BF, 0, 64))
+    # without one the output decides, and without either the default does
+    assert gn.gn_rms_forward(x, w, out=e(F32, 0, 64))[0].dtype == F32 and gn.gn_rms_forward(x, w)[0].dtype == BF
+    assert gn.gn_rms_forward_q8(x, w, out=e(E4, 0, 64))[0].dtype == E4 and gn.gn_rms_forward_q8(x, w)[0].dtype == torch.int8
+    assert gn.gn_rms_forward_q8(x, w, q_dtype=E4)[0].dtype == E4
+    q = e(torch.int8, 0, 64)
+    assert gn.gn_q8_dequantize(q, scale, out=e(BF, 0, 64)).dtype == BF and gn.gn_q8_dequantize(q, scale).dtype == F32
+    assert gn.gn_q8_dequantize(q, scale, BF, out=e(BF, 0, 64)).dtype == BF

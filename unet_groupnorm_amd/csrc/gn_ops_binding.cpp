@@ -181,6 +181,12 @@ at::Tensor rstd_of(const at::Tensor& x, const OptTensor& rstd, bool need)
     return need ? fresh(lead(x), at::kFloat, x) : at::Tensor();
 }
 
+// The dtype asked for (negative: none) and that of the output given.
+void agree(const char* name, int asked, int given)
+{
+    if (asked >= 0 && asked != given) throw py::type_error(std::string(name) + " is not the dtype of the given output");
+}
+
 py::tuple rms_forward(const at::Tensor& x, const OptTensor& weight, double eps, const OptTensor& residual,
                       int out_code, bool need_rstd, const OptTensor& out, const OptTensor& h_out,
                       const OptTensor& rstd_out)
@@ -189,6 +195,7 @@ py::tuple rms_forward(const at::Tensor& x, const OptTensor& weight, double eps, 
     const at::Tensor y = out.has_value() ? *out : fresh(x.sizes(), out_code < 0 ? x.scalar_type() : type_of_code(out_code), x);
     void* yp = like("out", y, x);
     const int yc = code_of(y, "out");
+    agree("out_dtype", out_code, yc);
     const at::Tensor h = h_of(x, residual, h_out), rstd = rstd_of(x, rstd_out, need_rstd);
     float* rp = rstd.defined() ? f32("rstd", rstd, in.r.T, in.didx) : nullptr;
     const int status = gn::rms_forward(x.data_ptr(), in.xc, in.r.stride, in.res, in.rc, in.w, in.wc, in.r.T, in.r.H,
@@ -205,9 +212,10 @@ py::tuple rms_forward_q8(const at::Tensor& x, const OptTensor& weight, double ep
     const Inputs in = inputs_of(x, weight, residual);
     const at::Tensor q = out.has_value()
                              ? *out
-                             : fresh(x.sizes(), q_dtype == GN_Q_INT8 ? at::kChar : at::kFloat8_e4m3fn, x);
+                             : fresh(x.sizes(), q_dtype == GN_Q_E4M3 ? at::kFloat8_e4m3fn : at::kChar, x);
     void* qp = like("out", q, x);
     const int qc = q_code_of(q);
+    agree("q_dtype", q_dtype, qc);
     const int64_t n = scales_of(in.r.H, block);
     const at::Tensor scale = scale_out.has_value() ? *scale_out : fresh(lead(x, n), at::kFloat, x);
     float* sp = f32("scale", scale, in.r.T * n, in.didx);
@@ -230,6 +238,7 @@ py::tuple q8_dequantize(const at::Tensor& q, const at::Tensor& scale, int out_co
         out.has_value() ? *out : fresh(q.sizes(), type_of_code(out_code < 0 ? GN_F32 : out_code), q);
     void* op = like("out", o, q);
     const int oc = code_of(o, "out");
+    agree("out_dtype", out_code, oc);
     const int status = gn::q8_dequantize(q.data_ptr(), qc, f32("scale", scale, r.T * scales_of(r.H, block), didx), r.T,
                                         r.H, block, op, oc, stream_of(didx), didx);
     mark_written(status, {&out});

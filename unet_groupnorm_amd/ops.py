@@ -40,7 +40,8 @@ def gn_rms_forward(x, weight, eps=1e-6, *, residual=None, out_dtype=None, need_r
                    rstd=None):
     """Returns (y, h, rstd): h = x + residual, rounded once to residual's dtype (x itself
     without a residual); rstd = 1 / sqrt(mean(h^2) + eps) over each row, fp32; y = h * rstd *
-    weight, computed in fp32 and rounded once to out_dtype (x.dtype by default, or float32).
+    weight, computed in fp32 and rounded once to out_dtype (x.dtype or float32; out's by default,
+    or x's).
 
     residual: x's dtype or float32. weight: x's dtype or float32, H elements in any shape, None for
     ones. h=residual updates the residual stream in place, out=x overwrites a contiguous x. rstd,
@@ -50,15 +51,15 @@ def gn_rms_forward(x, weight, eps=1e-6, *, residual=None, out_dtype=None, need_r
     return y, h, rstd
 
 
-def gn_rms_forward_q8(x, weight, eps=1e-6, *, residual=None, q_dtype=torch.int8, block=0, need_rstd=False, out=None,
+def gn_rms_forward_q8(x, weight, eps=1e-6, *, residual=None, q_dtype=None, block=0, need_rstd=False, out=None,
                       scale=None, h=None, rstd=None):
-    """Returns (q, scale, h, rstd): gn_rms_forward's y in 8 bits (torch.int8, or
-    torch.float8_e4m3fn) with an fp32 scale for each row (block=0) or each run of 32, 64 or
-    128 columns: scale = max|y| / qmax, q = round(y / scale), qmax 127 or 448. scale has x's
-    leading sizes and one more dimension, the scales of a row. A run that holds a NaN or an
-    infinity has a NaN scale and zeros."""
+    """Returns (q, scale, h, rstd): gn_rms_forward's y in 8 bits (torch.int8 or
+    torch.float8_e4m3fn; out's dtype by default, or int8) with an fp32 scale for each row
+    (block=0) or each run of 32, 64 or 128 columns: scale = max|y| / qmax, q = round(y /
+    scale), qmax 127 or 448. scale has x's leading sizes and one more dimension, the scales of
+    a row. A run that holds a NaN or an infinity has a NaN scale and zeros."""
     try:
-        code = _Q[q_dtype]
+        code = -1 if q_dtype is None else _Q[q_dtype]
     except (KeyError, TypeError):
         raise TypeError(f"unsupported 8-bit dtype {q_dtype} (int8 or float8_e4m3fn)") from None
     q, scale, h, rstd, status = _gnbind.rms_forward_q8(x, weight, eps, residual, code, int(block), need_rstd, out,
@@ -67,9 +68,9 @@ def gn_rms_forward_q8(x, weight, eps=1e-6, *, residual=None, q_dtype=torch.int8,
     return q, scale, h, rstd
 
 
-def gn_q8_dequantize(q, scale, out_dtype=torch.float32, *, block=0, out=None):
-    """q * scale in out_dtype: the values that gn_rms_forward_q8's output stands for, for a
-    consumer without an 8-bit form."""
+def gn_q8_dequantize(q, scale, out_dtype=None, *, block=0, out=None):
+    """q * scale in out_dtype (out's by default, or float32): the values that
+    gn_rms_forward_q8's output stands for, for a consumer without an 8-bit form."""
     v, status = _gnbind.q8_dequantize(q, scale, _out_code(out_dtype), int(block), out)
     _check("gn_q8_dequantize", status)
     return v
