@@ -355,3 +355,17 @@ def test_a_dtype_that_contradicts_the_given_output_is_refused():
     q = e(torch.int8, 0, 64)
     assert gn.gn_q8_dequantize(q, scale, out=e(BF, 0, 64)).dtype == BF and gn.gn_q8_dequantize(q, scale).dtype == F32
     assert gn.gn_q8_dequantize(q, scale, BF, out=e(BF, 0, 64)).dtype == BF
+
+
+def test_layouts_of_clipped_outputs():
+    """Dimensions of one element have no say in a layout."""
+    g = torch.ones(4, 1, 3)
+    same = [torch.empty_strided((4, 1, 3), st) for st in ((3, 3, 1), (3, 1, 1), (3, 77, 1))]
+    t = torch.empty_strided((4, 1, 3), (1, 4, 4)), torch.empty_strided((4, 1, 3), (1, 9, 4))
+    for a, b in [(g, o) for o in same] + [(o, g) for o in same] + [t, t[::-1]] + [(torch.ones(1, 1), torch.ones(1, 1).t())]:
+        with pytest.raises(GnError) as e:                     # as far as the device check
+            gn.gn_grad_clip([a], 1.0, out=[b])
+        assert e.value.status == 8
+    for a, b in ((g, t[0]), (t[1], g), (torch.ones(2, 3), torch.ones(3, 2).t())):
+        with pytest.raises(ValueError):
+            gn.gn_grad_clip([a], 1.0, out=[b])

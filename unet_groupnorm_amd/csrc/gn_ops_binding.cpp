@@ -323,6 +323,16 @@ void dense(const at::Tensor& t, const char* name, int didx)
     if (t.get_device() != didx) throw py::value_error(std::string(name) + " must be on one device");
 }
 
+// Whether tensors of one shape hold their elements in one order: the strides of dimensions of
+// one element do not count, nor any of an empty tensor.
+bool same_order(const at::Tensor& a, const at::Tensor& b)
+{
+    if (a.numel() == 0 || a.strides() == b.strides()) return true;
+    for (int64_t i = 0; i < a.dim(); ++i)
+        if (a.size(i) != 1 && a.stride(i) != b.stride(i)) return false;
+    return true;
+}
+
 // The list of `grads` (each with its output where `out` is given; in place where clip is
 // set without one), the norm and, where asked for, the scaled tensors.
 py::tuple grads(const std::vector<at::Tensor>& g, const c10::optional<std::vector<at::Tensor>>& out, bool clip,
@@ -341,8 +351,7 @@ py::tuple grads(const std::vector<at::Tensor>& g, const c10::optional<std::vecto
         if (out.has_value()) {
             const at::Tensor& o = (*out)[i];
             dense(o, "out", didx);
-            if (o.sizes() != g[i].sizes() || (o.strides() != g[i].strides() && o.numel() > 1 &&
-                                              !(o.is_contiguous() && g[i].is_contiguous())))
+            if (o.sizes() != g[i].sizes() || !same_order(o, g[i]))
                 throw py::value_error("out must have the gradients' shapes and layouts");
             t[i].out = o.data_ptr();
             t[i].out_dtype = code_of(o, "out");

@@ -150,7 +150,7 @@ def gn_grad_norm(grads, norm_type=2.0, *, norm=None, workspace=None):
 
 def gn_grad_clip(grads, max_norm, norm_type=2.0, *, out=None, norm=None, workspace=None):
     """Scales the tensors by min(1, max_norm / (norm + 1e-6)), in place or into `out` (tensors
-    of the same shapes and layouts, in the gradients' dtype or float32), and returns the norm
+    of the same shapes and element orders, in the gradients' dtype or float32), and returns the norm
     from before. The factor is decided on the device."""
     v, status = _gnbind.grads(list(grads), None if out is None else list(out), True, float(max_norm),
                               _norm_code(norm_type), norm, workspace)
@@ -161,7 +161,8 @@ def gn_grad_clip(grads, max_norm, norm_type=2.0, *, out=None, norm=None, workspa
 def clip_gradients(parameters, max_norm, norm_type=2.0):
     """Clips the gradients of the parameters (a tensor or an iterable; those without a
     gradient are passed over) in place by their norm together, which is returned. A parameter
-    listed twice counts once."""
+    listed twice counts once. The gradients are dense, on one device (gradients on several are
+    refused), and none overlaps another."""
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = list({id(p): p.grad for p in parameters if p.grad is not None}.values())
     if not grads:
