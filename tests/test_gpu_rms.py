@@ -15,6 +15,7 @@ from unet_groupnorm_amd.gn import GnError
 pytestmark = pytest.mark.gpu
 BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 EPS = 1e-6
+INF = float("inf")
 
 
 def say(msg):
@@ -496,6 +497,24 @@ def test_autograd_partial_uses():
         y = gn.rms_norm(x, w)
         (g,) = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
         g.float().sum().backward()
+
+
+def test_autograd_of_the_stream_alone_beside_special_values():
+    """Where only h is used its gradient is x's and the residual's, whatever the rows hold."""
+    for x_dt, r_dt in ((BF, BF), (F16, F32), (F32, F32)):
+        x, res = rand((5, 64), x_dt, 150), rand((5, 64), r_dt, 151)
+        x[1, 3], x[2, 5], x[3] = float("nan"), INF, 0.0
+        res[3] = 0.0
+        x.requires_grad_(), res.requires_grad_()
+        w = rand((64,), F32, 152).requires_grad_()
+        dh = rand((5, 64), r_dt, 153)
+        _, h = gn.rms_norm(x, w, 0.0, residual=res)
+        h.backward(dh)
+        assert torch.equal(bits(res.grad), bits(dh)) and torch.equal(bits(x.grad), bits(dh.to(x_dt)))
+        assert float(w.grad.abs().max()) == 0
+        _, h = gn.rms_norm(x, None, 0.0, residual=res.detach())
+        (g,) = torch.autograd.grad(h, x, dh)
+        assert torch.equal(bits(g), bits(dh.to(x_dt)))
 
 
 @pytest.mark.parametrize("shape", [(1, 64), (1, 1, 64), (64, 1)], ids=str)

@@ -111,7 +111,7 @@ class RmsNormFn(torch.autograd.Function):
         y, h, rstd = gn_rms_forward(x, weight, eps, residual=residual, out_dtype=out_dtype)
         ctx.save_for_backward(h, rstd, weight)
         ctx.set_materialize_grads(False)
-        ctx.x_dtype, ctx.y_dtype, ctx.has_residual = x.dtype, y.dtype, residual is not None
+        ctx.x_dtype, ctx.has_residual = x.dtype, residual is not None
         return (y, h) if ctx.has_residual else y
 
     @staticmethod
@@ -121,9 +121,11 @@ class RmsNormFn(torch.autograd.Function):
             return None, None, None, None, None
         h, rstd, weight = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dy = torch.zeros(h.shape, dtype=ctx.y_dtype, device=h.device) if dy is None else dy.contiguous()
+        if dy is None:  # the stream alone: the norm has no part, also where a row is not finite
+            return (dh.to(ctx.x_dtype) if need[0] else None, torch.zeros_like(weight) if need[1] else None, None,
+                    dh if need[3] else None, None)
         dx, dweight, dres = gn_rms_backward(
-            dy, h, rstd, weight, dh=None if dh is None else dh.contiguous(), x_dtype=ctx.x_dtype, need_dx=need[0],
+            dy.contiguous(), h, rstd, weight, dh=None if dh is None else dh.contiguous(), x_dtype=ctx.x_dtype, need_dx=need[0],
             need_dres=ctx.has_residual and need[3], need_dweight=weight is not None and need[1])
         return dx, dweight, None, dres, None
 
