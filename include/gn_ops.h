@@ -146,7 +146,8 @@ int gn_grad_norm(const gn_grad_tensor* tensors, int64_t n, int norm_type, float*
  *   out = data * coef,  coef = min(1, max_norm / (norm + 1e-6)),
  * coef taken in fp64 and rounded to fp32, the product rounded once to out_dtype. coef is
  * decided on the device: nothing waits for the norm. A NaN norm makes every output NaN; an
- * infinite one makes coef 0. In place with coef == 1 the tensors are left as they are.
+ * infinite one makes coef 0, unless max_norm is infinite too: that clips nothing, coef is 1.
+ * In place with coef == 1 the tensors are left as they are.
  * Outputs may not overlap one another or another tensor's data (a tensor listed twice).
  */
 int gn_grad_clip(const gn_grad_tensor* tensors, int64_t n, int norm_type, double max_norm, float* norm,

@@ -181,6 +181,22 @@ def test_nan_and_infinity(kind):
                 assert float(t[0].abs().max()) == 0 and bool(torch.isnan(t[1][place])) and int(torch.isnan(t[1]).sum()) == 1
 
 
+@pytest.mark.parametrize("n", [1000, 26_000_001])
+def test_an_infinite_limit_clips_nothing(n):
+    """Whatever the norm is, infinity among it; a NaN norm still makes every output NaN."""
+    for bad in (1.0, INF, -INF):
+        t = [rand(100, BF, 1), rand(n, F32, 2)]
+        t[1][7] = bad
+        kept, outs = [v.clone() for v in t], [torch.empty_like(v) for v in t]
+        for kind in (2.0, INF):
+            norm = gn.gn_grad_clip(t, INF, kind, out=outs)
+            assert torch.equal(gn.gn_grad_clip(t, INF, kind), norm) and (math.isinf(float(norm)) == math.isinf(bad))
+            for a, b, o in zip(t, kept, outs):
+                assert torch.equal(bits(a), bits(b)) and torch.equal(bits(o), bits(b))
+    t[1][7] = float("nan")
+    assert math.isnan(float(gn.gn_grad_clip(t, INF))) and all(bool(torch.isnan(v).all()) for v in t)
+
+
 def test_layouts_and_refusals():
     conv = torch.randn(8, 4, 3, 3, 3, device="cuda").contiguous(memory_format=torch.channels_last_3d)
     t = conv.clone(memory_format=torch.preserve_format)

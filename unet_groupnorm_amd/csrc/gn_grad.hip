@@ -220,9 +220,10 @@ __device__ __forceinline__ void step_scale(const T* p, O* o, int n, float coef)
         [&](int i, float v) { Io<O>::store1(o + i, v * coef); });
 }
 
-// coef from the norm; a NaN stays.
+// coef from the norm; a NaN stays. An infinite max_norm clips nothing, an infinite norm neither.
 __device__ __forceinline__ float coef_of(double norm, double max_norm)
 {
+    if (max_norm == __builtin_huge_val() && norm == norm) return 1.0f;
     const double c = max_norm / (norm + 1e-6);
     return c >= 1.0 ? 1.0f : float(c);
 }
