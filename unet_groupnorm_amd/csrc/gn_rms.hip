@@ -280,12 +280,15 @@ q8_dequantize_kernel(const uint8_t* q, int q_dtype, const float* scale, int64_t 
 template <typename XT, typename RT, int W>
 hipError_t fwd(const RmsArgs& a, bool q8, const RowPlan& p, hipStream_t st)
 {
+    // 16-bit inputs in pieces of 4 have an fp32 output, or an fp32 residual
+    constexpr bool kQ8 = W == 8 || sizeof(XT) == 4 || std::is_same<RT, float>::value;
     const dim3 grid = dim3(unsigned((a.T + p.rows - 1) / p.rows));
     return with_row<W>(p, a.H, [&](auto v, auto end) {
         constexpr int V = decltype(v)::value;
         constexpr int E = decltype(end)::value;
-        return q8 ? launch(rms_fwd_kernel<XT, RT, W, V, E, true>, grid, dim3(p.block), st, a)
-                  : launch(rms_fwd_kernel<XT, RT, W, V, E, false>, grid, dim3(p.block), st, a);
+        if constexpr (kQ8)
+            if (q8) return launch(rms_fwd_kernel<XT, RT, W, V, E, true>, grid, dim3(p.block), st, a);
+        return q8 ? hipErrorInvalidValue : launch(rms_fwd_kernel<XT, RT, W, V, E, false>, grid, dim3(p.block), st, a);
     });
 }
 
