@@ -3,6 +3,7 @@ symbol is exported, invalid arguments are refused with the documented status bef
 touches the device, and the binding refuses tensors of the wrong sizes, dtypes or layouts."""
 import ctypes
 import os
+import random
 import re
 
 import pytest
@@ -369,3 +370,76 @@ def test_layouts_of_clipped_outputs():
     for a, b in ((g, t[0]), (t[1], g), (torch.ones(2, 3), torch.ones(3, 2).t())):
         with pytest.raises(ValueError):
             gn.gn_grad_clip([a], 1.0, out=[b])
+
+
+# ------------------------------------------------------------------ lists against their definition
+
+SIZE = {GN_F32: 4, GN_BF16: 2, GN_F16: 2}
+
+
+def meets(a, b):
+    return a[0] < b[1] and b[0] < a[1] and a[0] < a[1] and b[0] < b[1]
+
+
+def overlaps(rows, norm, ws):
+    """The definition, pair by pair: no output meets another output, another tensor's data, or its
+    own data except in its place; the norm and the workspace meet nothing."""
+    spans = [((d, d + n * SIZE[dt]), (o, o + n * SIZE[odt]), dt == odt) for d, o, n, dt, odt in rows]
+    for i, (d, o, same) in enumerate(spans):
+        if meets(o, d) and not (o == d and same):
+            return True
+        for k, (d2, o2, _) in enumerate(spans):
+            if k != i and (meets(o, o2) or meets(o, d2)):
+                return True
+    return meets(norm, ws) or any(meets(s, b) for d, o, _ in spans for s in (d, o) for b in (norm, ws))
+
+
+def partials(sizes):
+    """Partial results of a list: a share of 2048 workgroups by tiles for each table of 160
+    entries of up to 2^27 elements, at most one for a step of 4 tiles of 2048."""
+    entries = [min(n - k, 1 << 27) for n in sizes for k in range(0, n, 1 << 27)]
+    tiles = [-(-n // 2048) for n in entries]
+    tables = [sum(tiles[k:k + 160]) for k in range(0, len(tiles), 160)] or [0]
+    total = max(sum(tiles), 1)
+    return sum(max(1, min(-(-t // 4), t * 2048 // total)) for t in tables)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_lists_against_the_definition(seed):
+    rng = random.Random(seed)
+    dense = seed % 3
+    for _ in range(60):
+        n, room = rng.choice([1, 2, 3, rng.randint(1, 12), rng.randint(1, 400)]), rng.choice([200, 4000, 1 << 20])
+        if dense == 2:
+            room *= 64                                      # mostly apart
+        rows, place = [], 0
+        for _ in range(n):
+            dt = rng.choice([GN_F32, GN_BF16, GN_F16])
+            odt, m = rng.choice([dt, GN_F32]), rng.choice([0, 1, 2, rng.randint(1, 40), rng.randint(1, 300)])
+            if dense == 0:                                  # one behind the other, as in a bucket
+                d, o = place, place + (n << 12)
+                place += m * 4
+            else:
+                d, o = rng.randrange(room) * 4, rng.randrange(room) * 4
+            if odt == dt and rng.random() < 0.4:
+                o = d
+            rows.append((0x10000000 + d, 0x10000000 + o, m, dt, odt))
+        if rng.random() < 0.5:
+            rng.shuffle(rows)
+        need = (partials([r[2] for r in rows]) + 1) * 8
+        far = rng.random() < 0.7
+        norm = 0x60000000 if far else 0x10000000 + rng.randrange(room) * 4
+        ws = 0x70000000 if far else 0x10000000 + rng.randrange(room) * 16
+        t = glist(*((ctypes.c_void_p(d), ctypes.c_void_p(o), m, dt, odt) for d, o, m, dt, odt in rows))
+        assert lib.gn_grad_workspace_bytes(t, n) == need
+        want = 33 if overlaps(rows, (norm, norm + 4), (ws, ws + need)) else 8      # 8: as far as the device check
+        assert lib.gn_grad_clip(t, n, 0, 1.0, norm, ws, need, None) == want, (seed, rows, norm, ws)
+        assert lib.gn_grad_clip(t, n, 0, 1.0, norm, ws, need - 1, None) == 6
+
+
+@pytest.mark.parametrize("sizes", [[], [0], [1], [8192], [8193], [1 << 27], [(1 << 27) + 1], [1 << 33], [5] * 160, [5] * 161,
+                                   [(1 << 27) + 1] * 100, [1 << 40, 3, 1 << 29], [1 << 48] + [1] * 200, [300_000_000] + [7] * 900],
+                         ids=lambda s: f"{len(s)} of {s[:1]}")
+def test_partials_of_long_lists(sizes):
+    t = glist(*((at(0), None, n, GN_BF16, GN_BF16) for n in sizes or [0]))
+    assert lib.gn_grad_workspace_bytes(t, len(sizes or [0])) == (partials(sizes) + 1) * 8
