@@ -5,12 +5,12 @@
 //
 // Bound by the bytes it moves (5 operations for 7 to 8 bytes): a row is read once into
 // registers, reduced there, and written once. Measured, bf16 with the residual, 8192 x 4096:
-// 41.7 us, 6.44 TB/s (a copy: 6.3; counted HBM bytes equal these); 4096 x 8192 to int8: 39 us,
-// 6.0 TB/s. One workgroup for each row of more than 512 columns, and no persistent ones: the
-// loads in flight are those of the other workgroups on the CU. Rows of 128 columns (131072 of them, 13.4 us, 5.0 TB/s) are
-// bound by their instructions; 4 rows a lane with one load of the weight gained 8% there and
-// lost as much at 65536 rows, and was not kept. One token (1 x 4096) takes 2.2 us on the GPU,
-// an empty launch's time, and 5 us of the host.
+// 41.7 us, 6.44 TB/s (a copy: 6.3; counted HBM bytes equal these); 4096 x 8192 to int8: 39.7 us,
+// 5.9 TB/s. One workgroup for each row of more than 512 columns, and no persistent ones: the
+// loads in flight are those of the other workgroups on the CU. Rows of 128 columns (131072 of
+// them, 13.0 us, 5.2 TB/s) are bound by their instructions; 4 rows a lane with one load of the
+// weight gained 8% there and lost as much at 65536 rows, and was not kept. One token (1 x 4096)
+// takes 2.0 us on the GPU, an empty launch's time, and 5 us of the host.
 #include <algorithm>
 
 #include "gn_rows.hpp"
