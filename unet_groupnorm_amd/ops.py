@@ -153,7 +153,7 @@ def gn_grad_norm(grads, norm_type=2.0, *, norm=None, workspace=None):
 def gn_grad_clip(grads, max_norm, norm_type=2.0, *, out=None, norm=None, workspace=None):
     """Scales the tensors by min(1, max_norm / (norm + 1e-6)), in place or into `out` (tensors
     of the same shapes and element orders, in the gradients' dtype or float32), and returns the norm
-    from before. The factor is decided on the device."""
+    from before. The factor is decided on the device; an infinite max_norm clips nothing."""
     v, status = _gnbind.grads(list(grads), None if out is None else list(out), True, float(max_norm),
                               _norm_code(norm_type), norm, workspace)
     _check("gn_grad_clip", status)
