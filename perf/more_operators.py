@@ -81,12 +81,8 @@ def draw(rng):
     if rng.random() < 0.6:
         H = max(64, H // 64 * 64)   # most widths are whole multiples of a head
     T = _log_int(rng, 1, min(65536, MAX_ELEMENTS // 2 // H))
-    # One vector for all rows, one for each of a few sequences, or one for each token.
-    kind = rng.choice(["one", "one", "few", "few", "token"])
-    if kind == "token":
-        T = max(1, T // 2)
-        samples = T
-    elif kind == "few":
+    # One vector for all rows, or one for each of a few sequences.
+    if rng.random() < 0.5:
         samples = _log_int(rng, 1, min(64, T))
         T = T // samples * samples
     else:
