@@ -1,0 +1,136 @@
+/*
+ * gn_join.h -- C ABI of libgn.so, third part: the join of a block's output into the residual
+ * stream (the norm after the block, its gate, the scales of both sides, and the norm before
+ * the next block) forward and backward, and 8-bit checkpoints of activations, which the join
+ * writes and its backward pass reads, on MI355X (gfx950).
+ *
+ * Ownership, ordering, devices and errors are those of gn_ops.h: the caller owns every buffer,
+ * nothing is allocated, synchronized or copied to the host, every check runs before anything
+ * is enqueued, and on any error other than GN_ERR_LAUNCH no output is touched. No call uses
+ * atomics: repeated calls give the same bits. A workspace needs no initialization and carries
+ * nothing from one call to the next; calls that may overlap in time need one each.
+ *
+ * Statuses are gn_status, gn_ops_status and gn_join_status codes; gn_ops_status_string
+ * describes all of them. Data types are gn_dtype codes, 8-bit formats gn_q8 codes.
+ */
+#ifndef GN_JOIN_H
+#define GN_JOIN_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gn_ops.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum gn_join_status {
+    GN_ERR_SAMPLES = 48, /* samples < 1 (< 0 without rows), T no multiple of it, or a stride of the
+                            gate or the scale that is neither 0 nor at least H */
+    GN_ERR_SCALE = 49,   /* residual_scale or branch_scale not finite */
+    GN_ERR_POST = 50     /* post_weight, post_rstd or dpost_weight without post_norm */
+} gn_join_status;
+
+/* ------------------------------------------------------------------ checkpoints
+ *
+ * An activation kept in 8 bits: for each row (block == 0) or each run of `block` columns (32,
+ * 64 or 128; a row's last may be shorter)
+ *   scale = max(max|x| / qmax, 2^-126),  q = x / scale rounded to nearest, ties to even,
+ * qmax = 127 (GN_Q_INT8) or 448 (GN_Q_E4M3), the scale the correctly rounded fp32 quotient and
+ * x / scale taken in fp32 to (1/2 + 2^-20) ulp. Where a run holds a NaN or an infinity its scale
+ * is NaN and its q are 0. gn_q8_dequantize reads it back.
+ *
+ * T rows of H columns (1 to GN_RMS_MAX_COLUMNS), x with row stride x_stride; q [T][H] and scale
+ * [T][ceil(H / block)] ([T] for block == 0) contiguous, of any alignment of their elements, and
+ * apart from x and each other. One kernel.
+ */
+int gn_q8_quantize(const void* x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int64_t block,
+                   void* q, int q_dtype, float* scale, void* stream);
+
+/* ------------------------------------------------------------------ join
+ *
+ * x is a block's output and residual the stream that it joins, T rows of H columns. The rows
+ * are those of `samples` sequences one behind the other, T / samples each; the gate and the
+ * scale hold a vector for each sequence, or one for all. With post_norm
+ *   post_rstd = 1 / sqrt(mean_i(x^2) + eps),     u = x * post_rstd * post_weight,
+ * else u = x, and
+ *   h    = residual_scale * residual + branch_scale * gate * u,   in fp32, rounded once to
+ *          r_dtype and stored: the new stream
+ *   rstd = 1 / sqrt(mean_i(h^2) + eps), of h as stored
+ *   y    = h * rstd * weight * (1 + scale), in fp32, rounded once.
+ * The vectors are combined first, in fp32: c = ((branch_scale * gate) * post_weight) and
+ * m = weight * (1 + scale); h is one fused multiply-add of (x * post_rstd) * c. With no
+ * post_norm, gate or scales of the two sides h, rstd and y are gn_rms_forward's bits.
+ *
+ * A NULL vector counts as ones (the scale as zeros). A row's results depend on that row, its
+ * vectors, H and the dtypes alone. A NaN or an infinity stays in its row. The means of squares
+ * are taken in fp32: H times them must stay below its maximum. T == 0 is legal.
+ */
+typedef struct gn_join {
+    int64_t T, H;           /* rows, columns (1 to GN_RMS_MAX_COLUMNS) */
+    int64_t samples;        /* sequences; 1 where gate and scale are one vector for all rows */
+    int64_t x_stride;       /* elements from one row of x to the next, at least H */
+    int64_t gate_stride;    /* elements from one sequence's gate to the next (>= H), or 0: one for all */
+    int64_t scale_stride;   /* the scale's likewise */
+    int64_t block;          /* columns of a checkpoint's scale: 0 (the row), 32, 64 or 128 */
+    int32_t x_dtype;        /* x, y, dy and dx */
+    int32_t r_dtype;        /* residual, h, dh and dres: x_dtype or GN_F32 */
+    int32_t w_dtype;        /* weight and dweight; each vector's type is x_dtype or GN_F32 */
+    int32_t post_dtype;     /* post_weight and dpost_weight */
+    int32_t gate_dtype;     /* gate and dgate */
+    int32_t scale_dtype;    /* scale and dscale */
+    int32_t post_norm;      /* 0: no norm after the block */
+    int32_t q_dtype;        /* format of the checkpoints */
+    float eps;
+    float residual_scale, branch_scale;
+} gn_join;
+
+/*
+ * Forward. y may be NULL (the stream alone: weight, scale and rstd are then not used). h may be
+ * residual itself, y may be x itself (x_stride == H); no other overlap with an output. rstd and
+ * post_rstd [T] may be NULL.
+ * h_q, h_scale and x_q, x_scale (each pair may be NULL): checkpoints of h as stored and of x,
+ * for gn_join_backward. One kernel.
+ */
+int gn_join_forward(const gn_join* j, const void* x, const void* residual, const void* weight,
+                    const void* post_weight, const void* gate, const void* scale, void* y, void* h, float* rstd,
+                    float* post_rstd, void* h_q, float* h_scale, void* x_q, float* x_scale, void* stream);
+
+/*
+ * Backward, from what the forward left: h and x in their types, or (h_scale not NULL) both
+ * as checkpoints, h and x then being the 8-bit tensors and every h and x below the fp32 values
+ * q * scale. dy (NULL: none) is y's gradient and dh (NULL: none) what reaches h by the stream.
+ * With m and c as above, xhat = h * rstd and xpost = x * post_rstd (x without post_norm),
+ *   d    = rstd * (dy * m - xhat * mean_i(dy * m * xhat)) + dh
+ *   dres = residual_scale * d
+ *   dx   = post_rstd * (d * c - xpost * mean_i(d * c * xpost))       (without post_norm d * c)
+ *   dscale[n]    = weight * A[n],                     A[n] = sum over n's rows of dy * xhat
+ *   dweight      = sum_n (1 + scale[n]) * A[n]
+ *   dgate[n]     = branch_scale * post_weight * C[n], C[n] = sum over n's rows of d * xpost
+ *   dpost_weight = sum_n branch_scale * gate[n] * C[n],
+ * the gate's and the scale's gradients summed over the sequences where they are one vector.
+ * Every output may be NULL. dgate and dscale are [samples][H] or, of one vector, [H], contiguous.
+ * Gradients of vectors are written, not accumulated, in their vector's type; they exist without
+ * the vector too (dpost_weight and dgate of NULL vectors in post_dtype and gate_dtype).
+ * The row mean of d * c * xpost is taken as mean((rstd * dy * m + dh) * c * xpost) less
+ * rstd * mean(dy * m * xhat) * mean(xhat * c * xpost), so that a row is reduced once.
+ *
+ * h and rstd are read where dy is given, x where there is post_norm or dgate is asked for
+ * (NULL otherwise allowed); dweight and dscale need no x. All sums are fp32 in a fixed order.
+ * dx may be dy, or x itself (x_stride == H); dres may be dh or h itself where the types agree;
+ * no other overlap. Only a call of no rows and no vector's gradient needs no workspace.
+ */
+size_t gn_join_workspace_bytes(int64_t T, int64_t H, int64_t samples);
+
+int gn_join_backward(const gn_join* j, const void* dy, const void* dh, const void* h, const float* h_scale,
+                     const void* x, const float* x_scale, const float* rstd, const float* post_rstd,
+                     const void* weight, const void* post_weight, const void* gate, const void* scale, void* dx,
+                     void* dres, void* dweight, void* dpost_weight, void* dgate, void* dscale, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GN_JOIN_H */

@@ -2,7 +2,8 @@
 statistics) behind a C ABI.
 
 Beside it the root-mean-square norm over rows with the residual's addition (also with an
-8-bit output), and the norm of many gradients with clipping.
+8-bit output), the norm of many gradients with clipping, the join of a block's output into the
+residual stream with the norms on both sides of it, and 8-bit checkpoints of activations.
 
 The kernels live in libgn.so (csrc/); this package is its torch binding.
 """
@@ -31,6 +32,16 @@ from .gn import (  # noqa: F401
     group_norm,
     layout_of,
     workspace_for,
+)
+from .join import (  # noqa: F401
+    JoinBackward,
+    JoinForward,
+    JoinNormFn,
+    gn_join_backward,
+    gn_join_forward,
+    gn_join_workspace_bytes,
+    gn_q8_quantize,
+    join_norm,
 )
 from .ops import (  # noqa: F401
     RmsNormFn,

@@ -20,6 +20,8 @@ STATUS_NAMES = {
 }
 # Status codes of include/gn_ops.h.
 OPS_STATUS_NAMES = {32: "GN_ERR_ROWS", 33: "GN_ERR_OVERLAP", 34: "GN_ERR_BLOCK", 35: "GN_ERR_NORM"}
+# Status codes of include/gn_join.h.
+JOIN_STATUS_NAMES = {48: "GN_ERR_SAMPLES", 49: "GN_ERR_SCALE", 50: "GN_ERR_POST"}
 # Size of the static scratch array that gn_forward_noalloc uses as its workspace.
 GN_NOALLOC_SCRATCH_BYTES = 1 << 20
 
@@ -32,6 +34,13 @@ class GnGradTensor(ctypes.Structure):
         ("dtype", ctypes.c_int32),
         ("out_dtype", ctypes.c_int32),
     ]
+
+
+class GnJoin(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("T", "H", "samples", "x_stride", "gate_stride", "scale_stride", "block")]
+                + [(n, ctypes.c_int32) for n in ("x_dtype", "r_dtype", "w_dtype", "post_dtype", "gate_dtype",
+                                                 "scale_dtype", "post_norm", "q_dtype")]
+                + [(n, ctypes.c_float) for n in ("eps", "residual_scale", "branch_scale")])
 
 
 class GnPlanInfo(ctypes.Structure):
@@ -117,6 +126,10 @@ def _declare(lib):
         "gn_q8_dequantize": (I, [P, I, P, I64, I64, I64, P, I, P]),
         "gn_rms_workspace_bytes": (SZ, [I64, I64]),
         "gn_rms_backward": (I, [P, I, P, I, I64, P, P, I, P, I64, I64, P, I, P, P, P, SZ, P]),
+        "gn_q8_quantize": (I, [P, I, I64, I64, I64, I64, P, I, P, P]),
+        "gn_join_forward": (I, [ctypes.POINTER(GnJoin)] + [P] * 15),
+        "gn_join_workspace_bytes": (SZ, [I64, I64, I64]),
+        "gn_join_backward": (I, [ctypes.POINTER(GnJoin)] + [P] * 19 + [SZ, P]),
         "gn_grad_workspace_bytes": (SZ, [ctypes.POINTER(GnGradTensor), I64]),
         "gn_grad_norm": (I, [ctypes.POINTER(GnGradTensor), I64, I, P, P, SZ, P]),
         "gn_grad_clip": (I, [ctypes.POINTER(GnGradTensor), I64, I, ctypes.c_double, P, P, SZ, P]),

@@ -221,11 +221,12 @@ py::tuple backward(const at::Tensor& dy, const at::Tensor& x, const c10::optiona
 
 }  // namespace
 
-void bind_ops(pybind11::module_& m);  // gn_ops_binding.cpp
+void bind_ops(pybind11::module_& m);   // gn_ops_binding.cpp
+void bind_join(pybind11::module_& m);  // gn_join_binding.cpp
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
 {
-    m.doc() = "Compiled marshalling of libgn.so's C ABI (GroupNorm's per-step calls, the row norm, gradients) for "
+    m.doc() = "Compiled marshalling of libgn.so's C ABI (GroupNorm's per-step calls, the row norm, gradients, the residual join) for "
               "torch tensors";
     m.def("forward", &forward, "gn_forward or gn_forward_cl: (y, mean, rstd, status, entry point)", py::arg("x"),
           py::arg("gamma"), py::arg("beta"), py::arg("G"), py::arg("eps"), py::arg("out_code"),
@@ -237,4 +238,5 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m)
           py::arg("workspace"), py::arg("dx"), py::arg("dgamma"), py::arg("dbeta"), py::arg("layout"));
     m.def("abi_version", []() { return gn_abi_version(); });
     bind_ops(m);
+    bind_join(m);
 }

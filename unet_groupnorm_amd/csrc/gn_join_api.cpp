@@ -1,0 +1,315 @@
+// gn_join_api.cpp -- the C ABI declared in include/gn_join.h: validation and launches.
+//
+// Every check runs before anything is enqueued. The library allocates nothing on the device,
+// never synchronizes, never reads device memory from the host and keeps no state.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "gn_args.hpp"
+#include "gn_join.h"
+#include "gn_join.hpp"
+#include "gn_join_internal.hpp"
+
+namespace {
+
+bool block_ok(int64_t b) { return b == 0 || b == 32 || b == 64 || b == 128; }
+bool q_ok(int q) { return q == GN_Q_INT8 || q == GN_Q_E4M3; }
+int64_t scales_of(int64_t H, int64_t block) { return block ? (H + block - 1) / block : 1; }
+
+// A vector of gn_join: its type, its alignment and the bytes it covers.
+struct Vec {
+    const void* p;
+    int64_t stride;
+    int dtype;
+    int64_t rows;  // vectors behind p
+    Span span(int64_t H) const { return Span(p, p ? rows_bytes(rows, H, stride, dtype) : 0); }
+};
+
+// Everything of j that does not depend on the direction. ckpt: checkpoints take part.
+int join_check(const gn_join* j, bool ckpt)
+{
+    if (!j) return GN_ERR_NULL;
+    if (const int rc = rows_check(j->T, j->H, j->x_stride)) return rc;
+    if (j->samples < (j->T ? 1 : 0) || j->samples > (int64_t(1) << 44) || (j->samples && j->T % j->samples)) return GN_ERR_SAMPLES;
+    for (const int64_t s : {j->gate_stride, j->scale_stride})
+        if (s && (s < j->H || s > (int64_t(1) << 58) / std::max<int64_t>(j->samples, 1))) return GN_ERR_SAMPLES;
+    const int x = j->x_dtype;
+    if (!dtype_ok(x) || !(j->r_dtype == x || j->r_dtype == GN_F32)) return GN_ERR_DTYPE;
+    for (const int d : {j->w_dtype, j->post_dtype, j->gate_dtype, j->scale_dtype})
+        if (!(d == x || d == GN_F32)) return GN_ERR_DTYPE;
+    if (ckpt && !q_ok(j->q_dtype)) return GN_ERR_DTYPE;
+    if (ckpt && !block_ok(j->block)) return GN_ERR_BLOCK;
+    if (!std::isfinite(j->eps) || j->eps < 0.0f) return GN_ERR_EPS;
+    if (!std::isfinite(j->residual_scale) || !std::isfinite(j->branch_scale)) return GN_ERR_SCALE;
+    return GN_OK;
+}
+
+Vec w_of(const gn_join* j, const void* p) { return Vec{p, 0, j->w_dtype, 1}; }
+Vec post_of(const gn_join* j, const void* p) { return Vec{p, 0, j->post_dtype, 1}; }
+Vec gate_of(const gn_join* j, const void* p)
+{
+    return Vec{p, j->gate_stride, j->gate_dtype, j->gate_stride ? j->samples : 1};
+}
+Vec scale_of(const gn_join* j, const void* p)
+{
+    return Vec{p, j->scale_stride, j->scale_dtype, j->scale_stride ? j->samples : 1};
+}
+gn::JoinVec vec(const Vec& v) { return gn::JoinVec{v.p, v.stride, v.dtype}; }
+
+gn::JoinVecs vecs_of(const gn_join* j, const void* w, const void* post, const void* gate, const void* scale)
+{
+    return gn::JoinVecs{vec(w_of(j, w)), vec(post_of(j, post)), vec(gate_of(j, gate)), vec(scale_of(j, scale)),
+                        j->branch_scale};
+}
+
+}  // namespace
+
+int gn::join_forward(const gn_join* j, const JoinForwardPtrs& p, void* stream, int device)
+{
+    const bool ckpt = p.h_q || p.h_scale || p.x_q || p.x_scale;
+    int rc = join_check(j, ckpt);
+    if (rc) return rc;
+    if (!j->post_norm && (p.post_weight || p.post_rstd)) return GN_ERR_POST;
+    const int64_t T = j->T, H = j->H;
+    if (T == 0) return GN_OK;
+    if (!p.x || !p.residual || !p.h || !p.h_q != !p.h_scale || !p.x_q != !p.x_scale) return GN_ERR_NULL;
+    const int64_t xs = size_of(j->x_dtype), rs = size_of(j->r_dtype), scales = scales_of(H, j->block);
+    const Vec w = w_of(j, p.y ? p.weight : nullptr), post = post_of(j, p.post_weight), gate = gate_of(j, p.gate),
+              scale = scale_of(j, p.y ? p.scale : nullptr);
+    for (const Vec& v : {w, post, gate, scale})
+        if (!aligned(v.p, size_of(v.dtype))) return GN_ERR_ALIGN;
+    if (!aligned(p.x, xs) || !aligned(p.residual, rs) || !aligned(p.y, xs) || !aligned(p.h, rs) || !aligned(p.rstd, 4) ||
+        !aligned(p.post_rstd, 4) || !aligned(p.h_scale, 4) || !aligned(p.x_scale, 4))
+        return GN_ERR_ALIGN;
+    float* rstd = p.y ? p.rstd : nullptr;
+    const Span sx(p.x, rows_bytes(T, H, j->x_stride, j->x_dtype)), sr(p.residual, T * H * rs);
+    const Span in[] = {sx, sr, w.span(H), post.span(H), gate.span(H), scale.span(H)};
+    const Span outs[] = {Span(p.y, T * H * xs), Span(p.h, T * H * rs), Span(rstd, T * 4), Span(p.post_rstd, T * 4),
+                         Span(p.h_q, T * H), Span(p.h_scale, T * scales * 4), Span(p.x_q, T * H),
+                         Span(p.x_scale, T * scales * 4)};
+    for (size_t k = 0; k < sizeof(outs) / sizeof(outs[0]); ++k) {
+        for (const Span& s : in) {
+            const bool place = (k == 0 && &s == &in[0] && p.y == p.x && j->x_stride == H) ||
+                               (k == 1 && &s == &in[1] && p.h == p.residual);
+            if (outs[k].meets(s) && !place) return GN_ERR_OVERLAP;
+        }
+        for (size_t i = 0; i < k; ++i)
+            if (outs[k].meets(outs[i])) return GN_ERR_OVERLAP;
+    }
+    OnDeviceOf dev(device);
+    if ((rc = dev.enter(p.x, stream)) ||
+        (rc = dev.holds({p.residual, w.p, post.p, gate.p, scale.p, p.y, p.h, rstd, p.post_rstd, p.h_q, p.h_scale, p.x_q,
+                         p.x_scale})))
+        return rc;
+    const gn::RowPlan plan = gn::row_plan(H, j->x_dtype == GN_F32 || j->r_dtype == GN_F32);
+    gn::JoinArgs a{};
+    a.v = vecs_of(j, w.p, post.p, gate.p, scale.p);
+    a.H = H;
+    a.x_stride = j->x_stride;
+    a.len = T / j->samples;
+    a.scales = scales;
+    a.eps = j->eps;
+    a.inv_H = 1.0f / float(H);
+    a.residual_scale = j->residual_scale;
+    a.lanes = plan.lanes;
+    a.rows = plan.rows;
+    a.q_dtype = j->q_dtype;
+    a.block = int32_t(j->block);
+    a.post = j->post_norm != 0;
+    a.one = j->samples == 1 || (!gate.stride && !scale.stride);
+    a.nt = T * H * (xs * (p.y ? 2 : 1) + 2 * rs + (p.h_q ? 1 : 0) + (p.x_q ? 1 : 0)) > gn::kRowStreamBytes;
+    for (int64_t t = 0; t < T; t += kMaxGroups * plan.rows) {
+        a.first = t;
+        a.T = std::min(T - t, kMaxGroups * plan.rows);
+        a.x = at(p.x, t * j->x_stride * xs);
+        a.res = at(p.residual, t * H * rs);
+        a.h = at(p.h, t * H * rs);
+        a.y = at(p.y, t * H * xs);
+        a.rstd = rstd ? rstd + t : nullptr;
+        a.post_rstd = p.post_rstd ? p.post_rstd + t : nullptr;
+        a.h_q = static_cast<uint8_t*>(at(p.h_q, t * H));
+        a.x_q = static_cast<uint8_t*>(at(p.x_q, t * H));
+        a.h_scale = p.h_scale ? p.h_scale + t * scales : nullptr;
+        a.x_scale = p.x_scale ? p.x_scale + t * scales : nullptr;
+        if (hipError_t e = gn::launch_join_fwd(a, j->x_dtype, j->r_dtype, plan, static_cast<hipStream_t>(stream)))
+            return launch_status(e);
+    }
+    return GN_OK;
+}
+
+int gn::join_backward(const gn_join* j, const JoinBackwardPtrs& p, void* stream, int device)
+{
+    const bool ckpt = p.h_scale || p.x_scale, vectors = p.dweight || p.dpost_weight || p.dgate || p.dscale;
+    int rc = join_check(j, ckpt);
+    if (rc) return rc;
+    if (!j->post_norm && (p.post_weight || p.post_rstd || p.dpost_weight)) return GN_ERR_POST;
+    const int64_t T = j->T, H = j->H, samples = j->samples;
+    if (T == 0 && !vectors) return GN_OK;
+    if (!p.workspace) return GN_ERR_NULL;
+    if (!aligned(p.workspace, 16)) return GN_ERR_ALIGN;
+    if (p.workspace_bytes < gn_join_workspace_bytes(T, H, samples)) return GN_ERR_WORKSPACE;
+    const Vec w = w_of(j, p.weight), post = post_of(j, p.post_weight), gate = gate_of(j, p.gate), scale = scale_of(j, p.scale);
+    const bool reads_x = j->post_norm || p.dgate, reads_h = p.dy != nullptr;
+    const int64_t xs = size_of(j->x_dtype), rs = size_of(j->r_dtype), scales = scales_of(H, j->block);
+    if (T > 0) {
+        if ((!p.dx && !p.dres && !vectors) || (reads_h && (!p.h || !p.rstd || (ckpt && !p.h_scale))) ||
+            (reads_x && (!p.x || (ckpt && !p.x_scale))) || (j->post_norm && !p.post_rstd))
+            return GN_ERR_NULL;
+        if (!ckpt && j->x_stride < H) return GN_ERR_ROWS;
+    }
+    for (const Vec& v : {w, post, gate, scale, w_of(j, p.dweight), post_of(j, p.dpost_weight), gate_of(j, p.dgate),
+                         scale_of(j, p.dscale)})
+        if (!aligned(v.p, size_of(v.dtype))) return GN_ERR_ALIGN;
+    if (!aligned(p.dy, xs) || !aligned(p.dh, rs) || (!ckpt && (!aligned(p.h, rs) || !aligned(p.x, xs))) ||
+        !aligned(p.h_scale, 4) || !aligned(p.x_scale, 4) || !aligned(p.rstd, 4) || !aligned(p.post_rstd, 4) ||
+        !aligned(p.dx, xs) || !aligned(p.dres, rs))
+        return GN_ERR_ALIGN;
+    const void *h = reads_h ? p.h : nullptr, *x = reads_x ? p.x : nullptr;
+    const int64_t x_stride = ckpt ? H : j->x_stride;
+    const gn::JoinSplit split = gn::join_split(T, samples);
+    const Span sdy(p.dy, T * H * xs), sdh(p.dh, T * H * rs), sh(h, T * H * (ckpt ? 1 : rs)),
+        sx(x, ckpt ? T * H : rows_bytes(T, H, x_stride, j->x_dtype));
+    const Span in[] = {sdy, sdh, sh, sx, Span(h ? p.h_scale : nullptr, T * scales * 4), Span(x ? p.x_scale : nullptr, T * scales * 4),
+                       Span(h ? p.rstd : nullptr, T * 4), Span(p.post_rstd, T * 4), w.span(H), post.span(H), gate.span(H),
+                       scale.span(H)};
+    const auto grad = [&](void* g, const Vec& v) { return Span(g, v.rows * H * size_of(v.dtype)); };
+    const Span outs[] = {Span(p.dx, T * H * xs), Span(p.dres, T * H * rs), grad(p.dweight, w), grad(p.dpost_weight, post),
+                         grad(p.dgate, gate), grad(p.dscale, scale),
+                         Span(p.workspace, int64_t(gn_join_workspace_bytes(T, H, samples)))};
+    for (size_t k = 0; k < sizeof(outs) / sizeof(outs[0]); ++k) {
+        for (size_t i = 0; i < sizeof(in) / sizeof(in[0]); ++i) {
+            // the same rows element for element
+            const bool place = (k == 0 && ((i == 0 && p.dx == p.dy) || (i == 3 && p.dx == x && !ckpt && x_stride == H))) ||
+                               (k == 1 && ((i == 1 && p.dres == p.dh) || (i == 2 && p.dres == h && !ckpt)));
+            if (outs[k].meets(in[i]) && !place) return GN_ERR_OVERLAP;
+        }
+        for (size_t i = 0; i < k; ++i)
+            if (outs[k].meets(outs[i])) return GN_ERR_OVERLAP;
+    }
+    OnDeviceOf dev(device);
+    if ((rc = dev.enter(p.workspace, stream)) ||
+        (T > 0 && (rc = dev.holds({p.dy, p.dh, h, x, h ? p.h_scale : nullptr, x ? p.x_scale : nullptr, h ? p.rstd : nullptr,
+                                   p.post_rstd, p.dx, p.dres}))) ||
+        (rc = dev.holds({w.p, post.p, gate.p, scale.p, p.dweight, p.dpost_weight, p.dgate, p.dscale})))
+        return rc;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const gn::JoinVecs v = vecs_of(j, w.p, post.p, gate.p, scale.p);
+    // the rows' means, then the partial sums
+    float2* row = static_cast<float2*>(p.workspace);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + (size_t(T) * sizeof(float2) + 15) / 16 * 16);
+    if (T > 0) {
+        gn::JoinBwdArgs a{};
+        a.dy = p.dy;
+        a.dh = p.dh;
+        a.h = h;
+        a.x = x;
+        a.h_scale = ckpt ? p.h_scale : nullptr;
+        a.x_scale = ckpt ? p.x_scale : nullptr;
+        a.rstd = p.rstd;
+        a.post_rstd = p.post_rstd;
+        a.dx = p.dx;
+        a.dres = p.dres;
+        a.v = v;
+        a.part = vectors ? part : nullptr;
+        a.row = row;
+        a.T = T;
+        a.H = H;
+        a.x_stride = x_stride;
+        a.len = split.len;
+        a.chunks = split.chunks;
+        a.split = split.split;
+        a.scales = scales;
+        a.inv_H = 1.0f / float(H);
+        a.residual_scale = j->residual_scale;
+        a.q_dtype = j->q_dtype;
+        a.block = int32_t(j->block);
+        a.post = j->post_norm != 0;
+        if (hipError_t e = gn::launch_join_bwd_rows(a, j->x_dtype, j->r_dtype, st)) return launch_status(e);
+    }
+    if (!vectors) return GN_OK;
+    gn::JoinVecGrads g{};
+    g.part = part;
+    g.dw = p.dweight;
+    g.dpost = p.dpost_weight;
+    g.dgate = p.dgate;
+    g.dscale = p.dscale;
+    g.v = v;
+    g.H = H;
+    g.chunks = T > 0 ? split.chunks : 0;
+    g.split = T > 0 ? split.split : 0;
+    g.samples = samples;
+    return launch_status(gn::launch_join_vectors(g, st));
+}
+
+int gn::q8_quantize(const void* x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int64_t block, void* q,
+                    int q_dtype, float* scale, void* stream, int device)
+{
+    int rc = rows_check(T, H, x_stride);
+    if (rc) return rc;
+    if (!dtype_ok(x_dtype) || !q_ok(q_dtype)) return GN_ERR_DTYPE;
+    if (!block_ok(block)) return GN_ERR_BLOCK;
+    if (T == 0) return GN_OK;
+    if (!x || !q || !scale) return GN_ERR_NULL;
+    if (!aligned(x, size_of(x_dtype)) || !aligned(scale, 4)) return GN_ERR_ALIGN;
+    const int64_t scales = scales_of(H, block);
+    const Span sx(x, rows_bytes(T, H, x_stride, x_dtype)), sq(q, T * H), ss(scale, T * scales * 4);
+    if (sq.meets(sx) || ss.meets(sx) || sq.meets(ss)) return GN_ERR_OVERLAP;
+    OnDeviceOf dev(device);
+    if ((rc = dev.enter(x, stream)) || (rc = dev.holds({q, scale}))) return rc;
+    const gn::RowPlan p = gn::row_plan(H, x_dtype == GN_F32);
+    gn::QuantArgs a{};
+    a.H = H;
+    a.x_stride = x_stride;
+    a.scales = scales;
+    a.lanes = p.lanes;
+    a.rows = p.rows;
+    a.q_dtype = q_dtype;
+    a.block = int32_t(block);
+    a.nt = T * H * (size_of(x_dtype) + 1) > gn::kRowStreamBytes;
+    for (int64_t t = 0; t < T; t += kMaxGroups * p.rows) {
+        a.T = std::min(T - t, kMaxGroups * p.rows);
+        a.x = at(x, t * x_stride * size_of(x_dtype));
+        a.q = static_cast<uint8_t*>(at(q, t * H));
+        a.scale = scale + t * scales;
+        if (hipError_t e = gn::launch_q8_quantize(a, x_dtype, p, static_cast<hipStream_t>(stream))) return launch_status(e);
+    }
+    return GN_OK;
+}
+
+extern "C" {
+
+int gn_q8_quantize(const void* x, int x_dtype, int64_t x_stride, int64_t T, int64_t H, int64_t block,
+                   void* q, int q_dtype, float* scale, void* stream)
+{
+    return gn::q8_quantize(x, x_dtype, x_stride, T, H, block, q, q_dtype, scale, stream, -1);
+}
+
+int gn_join_forward(const gn_join* j, const void* x, const void* residual, const void* weight,
+                    const void* post_weight, const void* gate, const void* scale, void* y, void* h, float* rstd,
+                    float* post_rstd, void* h_q, float* h_scale, void* x_q, float* x_scale, void* stream)
+{
+    return gn::join_forward(j, {x, residual, weight, post_weight, gate, scale, y, h, rstd, post_rstd, h_q, h_scale, x_q,
+                                x_scale}, stream, -1);
+}
+
+size_t gn_join_workspace_bytes(int64_t T, int64_t H, int64_t samples)
+{
+    if (rows_check(T, H, H) || samples < (T ? 1 : 0) || (samples && T % samples)) return 0;
+    const size_t rows = (size_t(T) * sizeof(float2) + 15) / 16 * 16;
+    return std::max<size_t>(rows + size_t(gn::join_split(T, samples).chunks) * size_t(H) * 2 * sizeof(float), 16);
+}
+
+int gn_join_backward(const gn_join* j, const void* dy, const void* dh, const void* h, const float* h_scale,
+                     const void* x, const float* x_scale, const float* rstd, const float* post_rstd,
+                     const void* weight, const void* post_weight, const void* gate, const void* scale, void* dx,
+                     void* dres, void* dweight, void* dpost_weight, void* dgate, void* dscale, void* workspace,
+                     size_t workspace_bytes, void* stream)
+{
+    return gn::join_backward(j, {dy, dh, h, h_scale, x, x_scale, rstd, post_rstd, weight, post_weight, gate, scale, dx,
+                                 dres, dweight, dpost_weight, dgate, dscale, workspace, workspace_bytes}, stream, -1);
+}
+
+}  // extern "C"

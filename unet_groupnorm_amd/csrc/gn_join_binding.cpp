@@ -1,0 +1,292 @@
+// gn_join_binding.cpp -- the compiled binding (Python module _gnbind) of include/gn_join.h for torch
+// tensors: the residual join and 8-bit checkpoints. Argument marshalling only, in the manner of
+// gn_ops_binding.cpp.
+#include <torch/extension.h>
+
+#include <cstdint>
+#include <string>
+
+#include "gn_join.h"
+#include "gn_join_internal.hpp"
+#include "gn_tensors.hpp"
+
+namespace {
+
+// A vector of H columns, or one for each of several sequences (rows of H, evenly spaced).
+struct Vectors {
+    const void* p = nullptr;
+    int64_t rows = 1, stride = 0;
+    int code = GN_F32;
+};
+
+Vectors vectors_of(const char* name, const OptTensor& v, int64_t T, int64_t H, int didx)
+{
+    Vectors out;
+    if (!v.has_value()) return out;
+    if (v->get_device() != didx) throw py::value_error(std::string(name) + " must be on x's device");
+    out.code = code_of(*v, name);
+    out.p = v->data_ptr();
+    if (v->numel() == H && v->is_contiguous()) return out;
+    const Rows r = rows_of(*v, name);
+    if (r.H != H || (r.T == 0 ? T != 0 : T % r.T != 0))
+        throw py::value_error(std::string(name) + " must have rows of x's columns, one or as many as divide x's rows");
+    if (r.T == 1) return out;
+    out.rows = r.T;
+    out.stride = r.stride;
+    return out;
+}
+
+struct Join {
+    gn_join j{};
+    Vectors gate, scale;
+    void *w = nullptr, *post = nullptr;
+};
+
+Join join_of(int64_t T, int64_t H, int x_code, int r_code, int didx, const OptTensor& weight, const OptTensor& post_weight,
+             const OptTensor& gate, const OptTensor& scale, bool post_norm, double residual_scale, double branch_scale)
+{
+    Join q;
+    q.gate = vectors_of("gate", gate, T, H, didx);
+    q.scale = vectors_of("scale", scale, T, H, didx);
+    if (q.gate.rows != 1 && q.scale.rows != 1 && q.gate.rows != q.scale.rows)
+        throw py::value_error("gate and scale must have as many rows, or one of them a single one");
+    q.j.T = T;
+    q.j.H = H;
+    q.j.samples = q.gate.rows != 1 ? q.gate.rows : q.scale.rows;
+    q.j.gate_stride = q.gate.stride;
+    q.j.scale_stride = q.scale.stride;
+    q.j.x_stride = H;
+    q.j.x_dtype = x_code;
+    q.j.r_dtype = r_code;
+    q.j.w_dtype = q.j.post_dtype = GN_F32;
+    q.j.gate_dtype = q.gate.code;
+    q.j.scale_dtype = q.scale.code;
+    if (weight.has_value()) {
+        q.j.w_dtype = code_of(*weight, "weight");
+        q.w = vec("weight", *weight, H, didx);
+    }
+    if (post_weight.has_value()) {
+        if (!post_norm) throw py::value_error("post_weight is given, but post_norm declines it");
+        q.j.post_dtype = code_of(*post_weight, "post_weight");
+        q.post = vec("post_weight", *post_weight, H, didx);
+    }
+    q.j.post_norm = post_norm;
+    q.j.residual_scale = float(residual_scale);
+    q.j.branch_scale = float(branch_scale);
+    return q;
+}
+
+at::ScalarType q_type(int q) { return q == GN_Q_E4M3 ? at::kFloat8_e4m3fn : at::kChar; }
+
+// The 8-bit tensor and the scales of a checkpoint of x.
+struct Checkpoint {
+    at::Tensor q, scale;
+    void* qp = nullptr;
+    float* sp = nullptr;
+};
+
+Checkpoint checkpoint_of(const at::Tensor& x, int64_t T, int64_t H, int q_dtype, int64_t block, const OptTensor& out,
+                         const OptTensor& scale_out)
+{
+    const int64_t n = scales_of(H, block);
+    Checkpoint c;
+    c.q = out.has_value() ? *out : fresh(x.sizes(), q_type(q_dtype), x);
+    c.qp = like("out", c.q, x);
+    c.scale = scale_out.has_value() ? *scale_out : fresh(lead(x, n), at::kFloat, x);
+    c.sp = f32("scale", c.scale, T * n, x.get_device());
+    return c;
+}
+
+py::object pair_of(const Checkpoint& c) { return c.q.defined() ? py::object(py::make_tuple(c.q, c.scale)) : py::none(); }
+
+py::tuple q8_quantize(const at::Tensor& x, int q_dtype, int64_t block, const OptTensor& out, const OptTensor& scale_out)
+{
+    const Rows r = rows_of(x, "x");
+    const int xc = code_of(x, "x"), didx = x.get_device();
+    const Checkpoint c = checkpoint_of(x, r.T, r.H, q_dtype, block, out, scale_out);
+    const int qc = q_code_of(c.q);
+    agree("q_dtype", q_dtype, qc);
+    const int status = gn::q8_quantize(x.data_ptr(), xc, r.stride, r.T, r.H, block, c.qp, qc, c.sp, stream_of(didx), didx);
+    mark_written(status, {&out, &scale_out});
+    return py::make_tuple(c.q, c.scale, status);
+}
+
+py::tuple join_forward(const at::Tensor& x, const at::Tensor& residual, const OptTensor& weight, double eps,
+                       const OptTensor& post_weight, const OptTensor& gate, const OptTensor& scale, bool post_norm,
+                       double residual_scale, double branch_scale, int q_dtype, int64_t block, bool saves_x, bool need_y,
+                       bool need_rstd, const OptTensor& out, const OptTensor& h_out, const OptTensor& rstd_out,
+                       const OptTensor& post_rstd_out, const OptTensor& h_q_out, const OptTensor& h_scale_out,
+                       const OptTensor& x_q_out, const OptTensor& x_scale_out)
+{
+    const Rows r = rows_of(x, "x");
+    const int didx = x.get_device(), xc = code_of(x, "x"), rc = code_of(residual, "residual");
+    Join q = join_of(r.T, r.H, xc, rc, didx, weight, post_weight, gate, scale, post_norm, residual_scale, branch_scale);
+    q.j.x_stride = r.stride;
+    q.j.eps = float(eps);
+    q.j.block = block;
+    q.j.q_dtype = q_dtype < 0 ? 0 : q_dtype;
+    wanted(out, need_y, "y");
+    if (rstd_out.has_value() && !need_y) throw py::value_error("rstd is given, but need_y declines it");
+    if (post_rstd_out.has_value() && !post_norm) throw py::value_error("post_rstd is given, but post_norm declines it");
+    gn::JoinForwardPtrs p{};
+    p.x = x.data_ptr();
+    p.residual = like("residual", residual, x);
+    p.weight = q.w;
+    p.post_weight = q.post;
+    p.gate = q.gate.p;
+    p.scale = q.scale.p;
+    at::Tensor y, rstd, post_rstd;
+    if (need_y) {
+        y = out.has_value() ? *out : fresh(x.sizes(), x.scalar_type(), x);
+        p.y = like("out", y, x);
+        if (y.scalar_type() != x.scalar_type()) throw py::type_error("out must have x's dtype");
+        rstd = rstd_of(x, rstd_out, need_rstd);
+        if (rstd.defined()) p.rstd = f32("rstd", rstd, r.T, didx);
+    }
+    const at::Tensor h = h_out.has_value() ? *h_out : fresh(x.sizes(), residual.scalar_type(), x);
+    p.h = like("h", h, x);
+    if (h.scalar_type() != residual.scalar_type()) throw py::type_error("h must have residual's dtype");
+    if (post_norm) {
+        post_rstd = rstd_of(x, post_rstd_out, need_rstd);
+        if (post_rstd.defined()) p.post_rstd = f32("post_rstd", post_rstd, r.T, didx);
+    }
+    Checkpoint ch, cx;
+    if ((h_q_out.has_value() && (q_dtype < 0 || !need_y)) || (x_q_out.has_value() && (q_dtype < 0 || !saves_x)))
+        throw py::value_error("a checkpoint's tensors are given, but the call leaves none of it");
+    if (q_dtype >= 0) {
+        if (need_y) {
+            ch = checkpoint_of(x, r.T, r.H, q_dtype, block, h_q_out, h_scale_out);
+            agree("checkpoint", q_dtype, q_code_of(ch.q));
+            p.h_q = ch.qp;
+            p.h_scale = ch.sp;
+        }
+        if (saves_x) {
+            cx = checkpoint_of(x, r.T, r.H, q_dtype, block, x_q_out, x_scale_out);
+            agree("checkpoint", q_dtype, q_code_of(cx.q));
+            p.x_q = cx.qp;
+            p.x_scale = cx.sp;
+        }
+    }
+    const int status = gn::join_forward(&q.j, p, stream_of(didx), didx);
+    mark_written(status, {&out, &h_out, &rstd_out, &post_rstd_out, &h_q_out, &h_scale_out, &x_q_out, &x_scale_out});
+    return py::make_tuple(or_none(y), h, or_none(rstd), or_none(post_rstd), pair_of(ch), pair_of(cx), status);
+}
+
+// A saved tensor of the backward pass: as it was, or a checkpoint with its scales.
+void saved(const char* name, const OptTensor& t, const OptTensor& scale, const at::Tensor& like_, const Rows& r, int64_t block,
+           int code, int didx, int* q_dtype, const void** p, const float** sp)
+{
+    if (!t.has_value()) return;
+    if (t->sizes() != like_.sizes()) throw py::value_error(std::string(name) + " must have the gradients' shape");
+    if (t->get_device() != didx) throw py::value_error(std::string(name) + " must be on the gradients' device");
+    *p = t->data_ptr();
+    if (scale.has_value()) {
+        if (!t->is_contiguous()) throw py::value_error(std::string(name) + "'s checkpoint must be contiguous");
+        const int q = q_code_of(*t);
+        if (*q_dtype >= 0 && *q_dtype != q) throw py::type_error("the checkpoints must have one format");
+        *q_dtype = q;
+        *sp = f32((std::string(name) + "'s scale").c_str(), *scale, r.T * scales_of(r.H, block), didx);
+    } else if (code_of(*t, name) != code) {
+        throw py::type_error(std::string(name) + " must have its gradient's dtype");
+    }
+}
+
+py::tuple join_backward(const OptTensor& dy, const OptTensor& dh, const OptTensor& h, const OptTensor& h_scale,
+                        const OptTensor& x, const OptTensor& x_scale, const OptTensor& rstd, const OptTensor& post_rstd,
+                        const OptTensor& weight, const OptTensor& post_weight, const OptTensor& gate,
+                        const OptTensor& scale, bool post_norm, double residual_scale, double branch_scale, int64_t block,
+                        int x_code, int r_code, bool need_dx, bool need_dres, bool need_dweight, bool need_dpost,
+                        bool need_dgate, bool need_dscale, const OptTensor& workspace, const OptTensor& dx_out,
+                        const OptTensor& dres_out, const OptTensor& dweight_out, const OptTensor& dpost_out,
+                        const OptTensor& dgate_out, const OptTensor& dscale_out)
+{
+    if (!dy.has_value() && !dh.has_value()) throw py::value_error("dy or dh must be given");
+    const at::Tensor& g = dy.has_value() ? *dy : *dh;
+    const Rows r = rows_of(g, dy.has_value() ? "dy" : "dh");
+    const int didx = g.get_device();
+    // x's and the stream's types: those of the gradients that are given, or as asked for
+    const int xc = dy.has_value() ? code_of(*dy, "dy") : x_code >= 0 ? x_code : code_of(*dh, "dh");
+    const int rc = dh.has_value() ? code_of(*dh, "dh") : r_code >= 0 ? r_code : xc;
+    if (x_code >= 0 && x_code != xc) throw py::type_error("x_dtype is not dy's dtype");
+    if (r_code >= 0 && r_code != rc) throw py::type_error("residual_dtype is not dh's dtype");
+    Join q = join_of(r.T, r.H, xc, rc, didx, weight, post_weight, gate, scale, post_norm, residual_scale, branch_scale);
+    q.j.eps = 0.0f;
+    q.j.block = block;
+    gn::JoinBackwardPtrs p{};
+    if (dy.has_value()) p.dy = like("dy", *dy, g);
+    if (dh.has_value()) p.dh = like("dh", *dh, g);
+    int q_dtype = -1;
+    const bool ckpt = h_scale.has_value() || x_scale.has_value();
+    if (ckpt && ((h.has_value() && !h_scale.has_value()) || (x.has_value() && !x_scale.has_value())))
+        throw py::value_error("h and x must both be tensors or both be checkpoints");
+    saved("h", h, h_scale, g, r, block, rc, didx, &q_dtype, &p.h, &p.h_scale);
+    saved("x", x, x_scale, g, r, block, xc, didx, &q_dtype, &p.x, &p.x_scale);
+    if (h.has_value() && !h->is_contiguous()) throw py::value_error("h must be contiguous");
+    if (x.has_value() && !ckpt) q.j.x_stride = rows_of(*x, "x").stride;
+    q.j.q_dtype = q_dtype < 0 ? 0 : q_dtype;
+    if (rstd.has_value()) p.rstd = f32("rstd", *rstd, r.T, didx);
+    if (post_rstd.has_value()) {
+        if (!post_norm) throw py::value_error("post_rstd is given, but post_norm declines it");
+        p.post_rstd = f32("post_rstd", *post_rstd, r.T, didx);
+    }
+    p.weight = q.w;
+    p.post_weight = q.post;
+    p.gate = q.gate.p;
+    p.scale = q.scale.p;
+    wanted(dx_out, need_dx, "dx");
+    wanted(dres_out, need_dres, "dres");
+    at::Tensor dx, dres, dw, dpost, dgate, dscale;
+    if (need_dx) {
+        dx = dx_out.has_value() ? *dx_out : fresh(g.sizes(), type_of_code(xc), g);
+        p.dx = like("dx", dx, g);
+        if (code_of(dx, "dx") != xc) throw py::type_error("dx must have x's dtype");
+    }
+    if (need_dres) {
+        dres = dres_out.has_value() ? *dres_out : fresh(g.sizes(), type_of_code(rc), g);
+        p.dres = like("dres", dres, g);
+        if (code_of(dres, "dres") != rc) throw py::type_error("dres must have the residual's dtype");
+    }
+    // a vector's gradient: the vector's shape and type, or without it H elements of fp32
+    const auto grad = [&](const char* name, bool need, const OptTensor& v, const OptTensor& given, at::Tensor* t) -> void* {
+        wanted(given, need, name);
+        if (!need) return nullptr;
+        *t = given.has_value() ? *given : v.has_value() ? fresh(v->sizes(), v->scalar_type(), g) : fresh({r.H}, at::kFloat, g);
+        if (t->scalar_type() != (v.has_value() ? v->scalar_type() : at::kFloat))
+            throw py::type_error(std::string(name) + " must have its vector's dtype");
+        return vec(name, *t, v.has_value() ? v->numel() : r.H, didx);
+    };
+    p.dweight = grad("dweight", need_dweight, weight, dweight_out, &dw);
+    p.dpost_weight = grad("dpost_weight", need_dpost, post_weight, dpost_out, &dpost);
+    p.dgate = grad("dgate", need_dgate, gate, dgate_out, &dgate);
+    p.dscale = grad("dscale", need_dscale, scale, dscale_out, &dscale);
+    const at::Tensor ws = workspace.has_value()
+                              ? *workspace
+                              : fresh({int64_t(gn_join_workspace_bytes(r.T, r.H, q.j.samples))}, at::kByte, g);
+    if (ws.get_device() != didx || !ws.is_contiguous())
+        throw py::value_error("workspace must be a contiguous tensor on the gradients' device");
+    p.workspace = ws.data_ptr();
+    p.workspace_bytes = size_t(ws.numel()) * ws.element_size();
+    const int status = gn::join_backward(&q.j, p, stream_of(didx), didx);
+    mark_written(status, {&dx_out, &dres_out, &dweight_out, &dpost_out, &dgate_out, &dscale_out});
+    return py::make_tuple(or_none(dx), or_none(dres), or_none(dw), or_none(dpost), or_none(dgate), or_none(dscale), status);
+}
+
+}  // namespace
+
+void bind_join(py::module_& m)
+{
+    m.def("q8_quantize", &q8_quantize, "gn_q8_quantize: (q, scale, status)", py::arg("x"), py::arg("q_dtype"),
+          py::arg("block"), py::arg("out"), py::arg("scale"));
+    m.def("join_forward", &join_forward, "gn_join_forward: (y, h, rstd, post_rstd, saved h, saved x, status)",
+          py::arg("x"), py::arg("residual"), py::arg("weight"), py::arg("eps"), py::arg("post_weight"), py::arg("gate"),
+          py::arg("scale"), py::arg("post_norm"), py::arg("residual_scale"), py::arg("branch_scale"), py::arg("q_dtype"),
+          py::arg("block"), py::arg("saves_x"), py::arg("need_y"), py::arg("need_rstd"), py::arg("out"), py::arg("h"),
+          py::arg("rstd"), py::arg("post_rstd"), py::arg("h_q"), py::arg("h_scale"), py::arg("x_q"), py::arg("x_scale"));
+    m.def("join_backward", &join_backward, "gn_join_backward: (dx, dres, dweight, dpost_weight, dgate, dscale, status)",
+          py::arg("dy"), py::arg("dh"), py::arg("h"), py::arg("h_scale"), py::arg("x"), py::arg("x_scale"),
+          py::arg("rstd"), py::arg("post_rstd"), py::arg("weight"), py::arg("post_weight"), py::arg("gate"),
+          py::arg("scale"), py::arg("post_norm"), py::arg("residual_scale"), py::arg("branch_scale"), py::arg("block"),
+          py::arg("x_code"), py::arg("r_code"), py::arg("need_dx"), py::arg("need_dres"), py::arg("need_dweight"),
+          py::arg("need_dpost"), py::arg("need_dgate"), py::arg("need_dscale"), py::arg("workspace"), py::arg("dx"),
+          py::arg("dres"), py::arg("dweight"), py::arg("dpost_weight"), py::arg("dgate"), py::arg("dscale"));
+}

@@ -13,7 +13,7 @@
 // takes 2.0 us on the GPU, an empty launch's time, and 5 us of the host.
 #include <algorithm>
 
-#include "gn_rows.hpp"
+#include "gn_q8.hpp"
 
 namespace gn {
 
@@ -21,136 +21,7 @@ namespace {
 
 constexpr int kRowMaxWaves = kRowMaxBlock / 64;
 
-// ------------------------------------------------------------------ 8 bits
-
-constexpr float kQMin = 0x1p-126f;  // smallest scale, the smallest normal fp32
-
-struct Scaled {
-    float scale, inv;  // inv: 1 / scale, within an ulp
-};
-
-// The scale of a run whose largest magnitude has the bits `amax`: a NaN where that is a NaN or
-// an infinity, else the quotient amax / qmax as a division rounds it. A product with 1 / qmax
-// and one correction by its remainder give that for every significand (both qmax checked over
-// all of them); the remainder is exact down to the floor's quotients.
-__device__ __forceinline__ Scaled scale_of(uint32_t amax, int q_dtype)
-{
-    if (amax >= 0x7f800000u) return Scaled{__uint_as_float(0x7fc00000u), 0.0f};
-    const float a = __uint_as_float(amax), d = q_dtype == GN_Q_INT8 ? 127.0f : 448.0f,
-                c = q_dtype == GN_Q_INT8 ? 1.0f / 127.0f : 1.0f / 448.0f, q = a * c;
-    const float s = fmaxf(fmaf(fmaf(-q, d, a), c, q), kQMin);
-    return Scaled{s, __builtin_amdgcn_rcpf(s)};  // s is a normal number
-}
-
-// v[e] = v[e] / scale. The product with the run's reciprocal is off by 2.5 ulp at most; its
-// remainder, exact but for 2^-25 of itself, corrects that to (1/2 + 2^-20) ulp of the quotient,
-// which is a division's result unless the quotient lies 2^-20 ulp from halfway between two
-// numbers. The remainder has to stay clear of fp32's smallest numbers: for scales from 2^-80 it
-// does wherever the quotient is not far below the formats' smallest steps. Smaller scales, and
-// a NaN, take the division itself (for all elements: 65536 x 512 bf16 to e4m3 by 32 28.0 us a
-// call against 22.5, 4096 x 8192 bf16 to int8 41.4 against 39.7).
-constexpr float kQDirect = 0x1p-80f;
-
-template <int W>
-__device__ __forceinline__ void divide(float (&v)[W], Scaled sc)
-{
-    if (sc.scale >= kQDirect) {
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const float q = v[e] * sc.inv;
-            v[e] = fmaf(fmaf(-q, sc.scale, v[e]), sc.inv, q);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = v[e] / sc.scale;
-    }
-}
-
-// Bits of the largest magnitude of a piece. The comparison is that of integers, which orders
-// a NaN above all numbers.
-template <int W>
-__device__ __forceinline__ uint32_t piece_amax(const float (&v)[W])
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < W; ++e) m = MaxBitsOp::f(m, __float_as_uint(v[e]) & 0x7fffffffu);
-    return m;
-}
-
-// 4 quotients, at most an ulp above qmax in magnitude, to 4 bytes: nearest, ties to even. For
-// int8 1.5 * 2^23 is added, which leaves the integer in the sum's low bits. `zero` (a run that
-// holds a NaN or an infinity) makes them 0.
-__device__ __forceinline__ uint32_t quantize4(const float* v, bool zero, int q_dtype)
-{
-    uint32_t q;
-    if (q_dtype == GN_Q_INT8) {
-        uint32_t b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(v[e] + 0x1.8p23f);
-        // byte 0 of each, first value lowest
-        q = __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
-                                  __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
-    } else {
-        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-        q = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true));
-    }
-    return zero ? 0u : q;
-}
-
-// W (4 or 8) values over the scale to their bytes lo to hi - 1.
-template <int W>
-__device__ __forceinline__ void store_q(uint8_t* p, int lo, int hi, float (&v)[W], Scaled sc, int q_dtype)
-{
-    uint32_t q[W / 4];
-    divide(v, sc);
-#pragma unroll
-    for (int k = 0; k < W / 4; ++k) q[k] = quantize4(v + 4 * k, sc.scale != sc.scale, q_dtype);
-    if (lo == 0 && hi == W) {
-        typedef uint32_t WordsAny __attribute__((ext_vector_type(W / 4), aligned(1)));
-        WordsAny t;
-#pragma unroll
-        for (int k = 0; k < W / 4; ++k) t[k] = q[k];
-        *reinterpret_cast<WordsAny*>(p) = t;
-    } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-            if (e >= lo && e < hi) p[e] = uint8_t((q[e / 4] >> (8 * (e & 3))) & 0xffu);
-    }
-}
-
 // ------------------------------------------------------------------ forward
-
-// 1 / sqrt(ss / H + eps) from an estimate r and v, the mean (a product with the rounded 1 / H,
-// corrected by its remainder) plus eps, each rounded once: p + lo = v * r exactly, so e = 1 - v
-// * r^2 is known to its last bits, and r + r * e / 2 is off by 3/8 e^2 of it before its one
-// rounding. An estimate of zero or infinity has no correction.
-__device__ __forceinline__ float inverse_rms(float ss, const RmsArgs& a)
-{
-    const float r = rsqrtf(fmaf(ss, a.inv_H, a.eps)), m = ss * a.inv_H;
-    const float v = fmaf(fmaf(-m, float(a.H), ss), a.inv_H, m) + a.eps;
-    const float p = v * r, lo = fmaf(v, r, -p), e = fmaf(-lo, r, fmaf(-p, r, 1.0f));
-    return r > 0.0f && r < __builtin_huge_valf() ? fmaf(0.5f * r, e, r) : r;
-}
-
-// One piece's output in 8 bits; `share` lanes share the scale, and the first of them stores it.
-template <int W, int END>
-__device__ __forceinline__ void store_q8(const RmsArgs& a, const Row<W>& r, int64_t t, int32_t i, int32_t share,
-                                         Scaled sc, float (&v)[W])
-{
-    if (END != kExact && (i > r.full || (i == r.full && !r.tail))) return;
-    const bool whole = END == kExact || i < r.full;
-    store_q<W>(out<uint8_t>(a.y) + t * a.H + (whole ? i * W : r.column(i)), whole || END == kTiny ? 0 : W - r.tail,
-               whole || END == kEnds ? W : r.H, v, sc, a.q_dtype);
-    if (a.block == 0 ? i == 0 : i % share == 0) a.scale[t * a.scales + (a.block == 0 ? 0 : i / share)] = sc.scale;
-}
-
-// Lanes that share a scale: the row's, or block / W neighbours (a row of fewer lanes than that
-// is one run).
-template <int W>
-__device__ __forceinline__ int32_t lanes_of_scale(const RmsArgs& a, const Row<W>& r)
-{
-    return a.block == 0 || a.block / W >= r.lanes ? r.lanes : a.block / W;
-}
 
 // Outputs are written after the sum's barrier: an output may take an input's place, and lanes
 // at the row's end read columns of others.
@@ -191,7 +62,7 @@ rms_fwd_kernel(RmsArgs a)
 #pragma unroll
         for (int u = 0; u < V; ++u) store_values<HT, W, END>(out<HT>(a.h) + t * a.H, r, r.piece(u), h[u]);
     }
-    const float rstd = inverse_rms(ss, a);
+    const float rstd = inverse_rms(ss, a.H, a.inv_H, a.eps);
     if (a.rstd && r.lane == 0) a.rstd[t] = rstd;
 #pragma unroll
     for (int u = 0; u < V; ++u)
@@ -206,7 +77,7 @@ rms_fwd_kernel(RmsArgs a)
             for (int u = 0; u < V; ++u) store_values<XT, W, END>(out<XT>(a.y) + t * a.H, r, r.piece(u), h[u]);
         }
     } else {
-        const int32_t share = lanes_of_scale(a, r);
+        const int32_t share = lanes_of_scale(a.block, r);
         uint32_t m[V];
 #pragma unroll
         for (int u = 0; u < V; ++u) m[u] = piece_amax(h[u]);
@@ -216,11 +87,12 @@ rms_fwd_kernel(RmsArgs a)
             m[0] = V > 1 || r.lanes > 64 ? row_all<MaxBitsOp, true>(m[0], r, s_max) : row_all<MaxBitsOp, false>(m[0], r, s_max);
             const Scaled sc = scale_of(m[0], a.q_dtype);
 #pragma unroll
-            for (int u = 0; u < V; ++u) store_q8<W, END>(a, r, t, r.piece(u), share, sc, h[u]);
+            for (int u = 0; u < V; ++u) store_q8<W, END>(out<uint8_t>(a.y) + t * a.H, a.scale + t * a.scales, a.block, r, r.piece(u), share, sc, a.q_dtype, h[u]);
         } else {
 #pragma unroll
             for (int u = 0; u < V; ++u)
-                store_q8<W, END>(a, r, t, r.piece(u), share, scale_of(lanes_all<MaxBitsOp>(m[u], share), a.q_dtype), h[u]);
+                store_q8<W, END>(out<uint8_t>(a.y) + t * a.H, a.scale + t * a.scales, a.block, r, r.piece(u), share,
+                                 scale_of(lanes_all<MaxBitsOp>(m[u], share), a.q_dtype), a.q_dtype, h[u]);
         }
     }
 }
@@ -254,18 +126,7 @@ q8_dequantize_kernel(const uint8_t* q, int q_dtype, const float* scale, int64_t 
             }
         }
         float v[W];
-#pragma unroll
-        for (int k = 0; k < W / 4; ++k) {
-            if (q_dtype == GN_Q_INT8) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[4 * k + e] = float(int8_t(b[k] >> (8 * e)));
-            } else {
-                v[4 * k] = __builtin_amdgcn_cvt_f32_fp8(int(b[k]), 0);
-                v[4 * k + 1] = __builtin_amdgcn_cvt_f32_fp8(int(b[k]), 1);
-                v[4 * k + 2] = __builtin_amdgcn_cvt_f32_fp8(int(b[k]), 2);
-                v[4 * k + 3] = __builtin_amdgcn_cvt_f32_fp8(int(b[k]), 3);
-            }
-        }
+        widen_q8(b, q_dtype, v);
 #pragma unroll
         for (int e = 0; e < W; ++e) v[e] = v[e] * s;
         Piece<OT, W> o;

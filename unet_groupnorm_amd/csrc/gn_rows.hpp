@@ -220,6 +220,18 @@ __device__ __forceinline__ float row_sum(float v, const Row<W>& r, uint32_t* s)
     return __uint_as_float(row_all<AddOp, MANY>(__float_as_uint(v), r, s));
 }
 
+// 1 / sqrt(ss / H + eps) from an estimate r and v, the mean (a product with the rounded 1 / H,
+// corrected by its remainder) plus eps, each rounded once: p + lo = v * r exactly, so e = 1 - v
+// * r^2 is known to its last bits, and r + r * e / 2 is off by 3/8 e^2 of it before its one
+// rounding. An estimate of zero or infinity has no correction.
+__device__ __forceinline__ float inverse_rms(float ss, int64_t H, float inv_H, float eps)
+{
+    const float r = rsqrtf(fmaf(ss, inv_H, eps)), m = ss * inv_H;
+    const float v = fmaf(fmaf(-m, float(H), ss), inv_H, m) + eps;
+    const float p = v * r, lo = fmaf(v, r, -p), e = fmaf(-lo, r, fmaf(-p, r, 1.0f));
+    return r > 0.0f && r < __builtin_huge_valf() ? fmaf(0.5f * r, e, r) : r;
+}
+
 // Calls f(pieces of a lane, how rows end) with a plan's values as constants.
 template <int W, typename F>
 hipError_t with_row(const RowPlan& p, int64_t H, F&& f)

@@ -1,0 +1,172 @@
+"""Torch binding of include/gn_join.h: the join of a block's output into the residual stream,
+with the norms after the block and before the next one, the gate and the scales, forward and
+backward; and 8-bit checkpoints of activations, which the join writes and its backward reads.
+
+Argument marshalling only, in the manner of ops.py: the functions have the names of the C entry
+points, the compiled module _gnbind checks the tensors, allocates what is not given and calls
+the library on the current stream of the tensors' device; a non-zero status becomes a GnError.
+
+A row is the last dimension, and x may be a view whose rows are evenly spaced. gate and scale are
+one vector of a row's columns, or a vector for each of several sequences: with S rows (evenly
+spaced; a slice of a wider projection will do) row t of x's T takes vector t // (T // S). Nothing
+here waits for the GPU. Tensors given to be written count as modified in place for autograd.
+"""
+from typing import NamedTuple, Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _gnbind
+from ._lib import lib
+from .gn import _out_code
+from .ops import _Q, _check
+
+Saved = Tuple[torch.Tensor, torch.Tensor]
+
+
+class JoinForward(NamedTuple):
+    """What gn_join_forward returns. saved_h and saved_x are checkpoints, (q, scale) each."""
+    y: Optional[torch.Tensor]
+    h: torch.Tensor
+    rstd: Optional[torch.Tensor]
+    post_rstd: Optional[torch.Tensor]
+    saved_h: Optional[Saved]
+    saved_x: Optional[Saved]
+
+
+class JoinBackward(NamedTuple):
+    """What gn_join_backward returns, None where not needed."""
+    dx: Optional[torch.Tensor]
+    dres: Optional[torch.Tensor]
+    dweight: Optional[torch.Tensor]
+    dpost_weight: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dscale: Optional[torch.Tensor]
+
+
+def _q_code(q_dtype):
+    try:
+        return -1 if q_dtype is None else _Q[q_dtype]
+    except (KeyError, TypeError):
+        raise TypeError(f"unsupported 8-bit dtype {q_dtype} (int8 or float8_e4m3fn)") from None
+
+
+def gn_q8_quantize(x, q_dtype=None, *, block=128, out=None, scale=None):
+    """Returns (q, scale): x in 8 bits (torch.int8 or torch.float8_e4m3fn; out's dtype by default,
+    or int8) with an fp32 scale for each row (block=0) or each run of 32, 64 or 128 columns, as
+    gn_rms_forward_q8's output. gn_q8_dequantize(q, scale, dtype, block=block) reads it back. A
+    run that holds a NaN or an infinity reads back as NaN."""
+    q, scale, status = _gnbind.q8_quantize(x, _q_code(q_dtype), int(block), out, scale)
+    _check("gn_q8_quantize", status)
+    return q, scale
+
+
+def gn_join_forward(x, residual, weight, eps=1e-6, *, post_weight=None, gate=None, scale=None, post_norm=None,
+                    residual_scale=1.0, branch_scale=1.0, checkpoint=None, block=128, need_y=True, need_rstd=True,
+                    out=None, h=None, rstd=None, post_rstd=None, saved_h=(None, None), saved_x=(None, None)):
+    """Returns a JoinForward: with u = x, or with post_norm (by default where post_weight is given)
+    u = x * post_rstd * post_weight,
+
+        h = residual_scale * residual + branch_scale * gate * u    (residual's dtype)
+        y = h * rstd * weight * (1 + scale)                        (x's dtype)
+
+    post_rstd and rstd being 1 / sqrt(mean(v^2) + eps) over each row of x and of h as stored, in
+    fp32. residual: x's dtype or float32; the vectors: x's dtype or float32 each, None for ones
+    (scale: zeros). h=residual updates the stream in place, out=x overwrites a contiguous x.
+    need_y=False leaves y, its weight and its scale out.
+
+    checkpoint (torch.int8 or torch.float8_e4m3fn): the kernel also leaves h in 8 bits, and x
+    where the backward pass reads it (there is post_norm or a gate), with scales as block says; pass
+    them to gn_join_backward in place of h and x, which need not be kept. saved_h and saved_x are
+    the tensors to write them into."""
+    if post_norm is None:
+        post_norm = post_weight is not None
+    *f, status = _gnbind.join_forward(
+        x, residual, weight, eps, post_weight, gate, scale, post_norm, residual_scale, branch_scale, _q_code(checkpoint),
+        block, post_norm or gate is not None, need_y, need_rstd, out, h, rstd, post_rstd, *saved_h, *saved_x)
+    _check("gn_join_forward", status)
+    return JoinForward(*f)
+
+
+def gn_join_workspace_bytes(T, H, samples=1):
+    """Bytes of gn_join_backward's workspace for T rows of H columns, `samples` sequences (rows of
+    the gate or of the scale)."""
+    return int(lib.gn_join_workspace_bytes(T, H, samples))
+
+
+def _pair(saved):
+    return saved if isinstance(saved, tuple) else (saved, None)
+
+
+def gn_join_backward(dy, h, rstd, weight, *, x=None, post_rstd=None, dh=None, post_weight=None, gate=None, scale=None,
+                     post_norm=None, residual_scale=1.0, branch_scale=1.0, block=128, x_dtype=None, residual_dtype=None,
+                     need_dx=True, need_dres=True, need_dweight=True, need_dpost_weight=None, need_dgate=None,
+                     need_dscale=None, workspace=None, dx=None, dres=None, dweight=None, dpost_weight=None, dgate=None,
+                     dscale=None):
+    """Returns a JoinBackward, from gn_join_forward's arguments and results. h and x are tensors or,
+    both, checkpoints: (q, scale) with the forward's block. x is read with post_norm (by default where
+    post_weight or post_rstd is given) or where the gate's gradient is needed. dy is y's gradient and
+    dh what reaches h by the stream; either may be None (h and rstd are then not read without dy).
+    dx and dres have dy's and dh's dtypes; x_dtype and residual_dtype say them where one is None (the
+    other's by default). Gradients of vectors have their vector's shape and dtype; they are needed
+    by default where the vector is given, the weights' also without (H float32 elements)."""
+    if post_norm is None:
+        post_norm = post_weight is not None or post_rstd is not None
+    h, h_scale = _pair(h)
+    x, x_scale = _pair(x)
+    need_dpost_weight = post_norm if need_dpost_weight is None else need_dpost_weight
+    need_dgate = gate is not None if need_dgate is None else need_dgate
+    need_dscale = scale is not None if need_dscale is None else need_dscale
+    *g, status = _gnbind.join_backward(
+        dy, dh, h, h_scale, x, x_scale, rstd, post_rstd, weight, post_weight, gate, scale, post_norm, residual_scale,
+        branch_scale, block, _out_code(x_dtype), _out_code(residual_dtype), need_dx, need_dres, need_dweight,
+        need_dpost_weight, need_dgate, need_dscale, workspace, dx, dres, dweight, dpost_weight, dgate, dscale)
+    _check("gn_join_backward", status)
+    return JoinBackward(*g)
+
+
+class JoinNormFn(torch.autograd.Function):
+    """(y, h) = the residual join with the HIP kernels in both directions; with a checkpoint dtype
+    what the backward pass reads is kept in 8 bits."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, post_weight, gate, scale, eps, post_norm, residual_scale, branch_scale,
+                checkpoint, block):
+        _gnbind.capture_check([x, residual, weight, post_weight, gate, scale])
+        x, gate, scale = (t if t is None or _gnbind.even_rows(t) else t.contiguous() for t in (x, gate, scale))
+        ctx.how = {"post_norm": post_norm, "residual_scale": residual_scale, "branch_scale": branch_scale, "block": block}
+        f = gn_join_forward(x, residual.contiguous(), weight, eps, post_weight=post_weight, gate=gate, scale=scale,
+                            checkpoint=checkpoint, **ctx.how)
+        reads_x = post_norm or gate is not None
+        kept = (*f.saved_h, *(f.saved_x or (None, None))) if checkpoint is not None else (f.h, None, x if reads_x else None, None)
+        ctx.save_for_backward(*kept, f.rstd, f.post_rstd, weight, post_weight, gate, scale)
+        ctx.set_materialize_grads(False)
+        ctx.dtypes = x.dtype, residual.dtype
+        return f.y, f.h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh):
+        if dy is None and dh is None:
+            return (None,) * 12
+        h, h_scale, x, x_scale, rstd, post_rstd, weight, post_weight, gate, scale = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        g = gn_join_backward(
+            dy if dy is None else dy.contiguous(), h if h_scale is None else (h, h_scale), rstd, weight,
+            x=x if x_scale is None else (x, x_scale), post_rstd=post_rstd, dh=dh if dh is None else dh.contiguous(),
+            post_weight=post_weight, gate=gate, scale=scale, x_dtype=ctx.dtypes[0], residual_dtype=ctx.dtypes[1],
+            need_dx=need[0], need_dres=need[1], need_dweight=weight is not None and need[2],
+            need_dpost_weight=post_weight is not None and need[3], need_dgate=gate is not None and need[4],
+            need_dscale=scale is not None and need[5], **ctx.how)
+        return (g.dx, g.dres, g.dweight, g.dpost_weight, g.dgate, g.dscale) + (None,) * 6
+
+
+def join_norm(x, residual, weight=None, eps=1e-6, *, post_weight=None, gate=None, scale=None, post_norm=None,
+              residual_scale=1.0, branch_scale=1.0, checkpoint=None, block=128):
+    """Joins a block's output x into the residual stream and norms the result for the next block,
+    differentiable in every tensor: returns (y, h) as gn_join_forward does. With a checkpoint dtype
+    (torch.int8 or torch.float8_e4m3fn) the graph keeps h and x in 8 bits instead of their own types,
+    and the gradients are those of the values that these stand for."""
+    post_norm = post_weight is not None if post_norm is None else bool(post_norm)
+    return JoinNormFn.apply(x, residual, weight, post_weight, gate, scale, eps, post_norm, float(residual_scale),
+                            float(branch_scale), checkpoint, int(block))

@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _gnbind
-from ._lib import GN_OK, OPS_STATUS_NAMES, STATUS_NAMES, lib
+from ._lib import GN_OK, JOIN_STATUS_NAMES, OPS_STATUS_NAMES, STATUS_NAMES, lib
 from .gn import _DT, GnError, _out_code
 
 _Q = {torch.int8: 0, torch.float8_e4m3fn: 1}
@@ -24,7 +24,7 @@ _NORM = {2: 0, 2.0: 0, float("inf"): 1}
 def _check(fn, status):
     if status != GN_OK:
         e = GnError(fn, status)
-        name = OPS_STATUS_NAMES.get(status) or STATUS_NAMES.get(status, status)
+        name = {**OPS_STATUS_NAMES, **JOIN_STATUS_NAMES, **STATUS_NAMES}.get(status, status)
         e.args = (f"{fn}: {name} ({lib.gn_ops_status_string(status).decode()})",)
         raise e
 
