@@ -1,6 +1,6 @@
 // gn_join.hpp -- kernel arguments, plans and launchers shared by gn_join_api.cpp and the kernel
-// files of the residual join (gn_join.hip, gn_join_bwd.hip) and of the 8-bit checkpoints
-// (gn_join.hip).
+// files of the residual join (gn_join.hip, gn_join_bwd.hip, gn_join_wide.hip) and of the 8-bit
+// checkpoints (gn_join.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -59,11 +59,10 @@ struct JoinBwdArgs {
     void* dres;       // null: none
     JoinVecs v;
     float* part;      // [2][chunks][H]: sums of dy * xhat, then of d * xpost; null: none
-    float2* row;      // two-kernel path: c1 * rstd and the mean of d * c * xpost of each row
+    float2* row;      // of wide rows: c1 * rstd and the mean of d * c * xpost of each row
     int64_t T, H, x_stride;
-    int64_t len;      // rows of a sequence
-    int64_t chunks;   // of all sequences together, `split` of each
-    int64_t split;
+    int64_t len, groups;    // rows and groups of a sequence
+    int64_t chunks, split;  // chunks of all sequences together and of each
     int64_t scales;
     float inv_H, residual_scale;
     int32_t lanes, rows;
@@ -72,39 +71,63 @@ struct JoinBwdArgs {
     bool nt;
 };
 
-// How the backward pass shares out the rows: every sequence is cut into `split` chunks, chunk k
-// taking the row groups k, k + split, ... of its sequence, and a workgroup takes whole chunks
-// and leaves two partial sums for each column of each.
-struct JoinSplit {
-    int64_t len, split, chunks;
+// How the backward pass shares out the rows. A row lies over lanes as in the row norm's backward;
+// `rows` of them are a group, which a workgroup takes at once. Every sequence is cut into `split`
+// chunks, chunk k taking the groups k, k + split, ... of its sequence; a workgroup takes whole
+// chunks and leaves two partial sums for each column of each. Rows of more than 16 columns a lane do
+// not fit (wide): they take two kernels, a thread of the second a few columns of a chunk.
+struct JoinPlan : RowPlan {
+    int64_t len, groups;     // rows and groups of a sequence
+    int64_t split, chunks;   // chunks of a sequence, of all
+    int64_t grid;            // workgroups
+    bool wide;
 };
 
-// Chunks of all sequences: as many as fill the chip's kBwdParts workgroups in whole turns as well
-// as up to eight turns can, and no more than there are rows.
-inline JoinSplit join_split(int64_t T, int64_t samples)
+// The chunks of a sequence of `groups` groups: as many as fill the chip's kBwdParts workgroups in
+// whole turns as well as up to eight turns can.
+inline int64_t join_split(int64_t groups, int64_t samples)
 {
-    JoinSplit s{samples > 0 ? T / samples : 0, 1, samples};
-    if (s.len < 2 || samples >= 8 * kBwdParts) return s;
+    if (groups < 2 || samples >= 8 * kBwdParts) return 1;
+    int64_t split = 1;
     double best = -1.0;
     for (int64_t turns = 1; turns <= 8; ++turns) {
         int64_t k = turns * kBwdParts / samples;
         if (k < 1) continue;
-        k = k < s.len ? k : s.len;
+        k = k < groups ? k : groups;
         const int64_t chunks = k * samples, rounds = (chunks + kBwdParts - 1) / kBwdParts;
         const double used = double(chunks) / double(rounds * kBwdParts);
         if (used > best + 0.03) {
             best = used;
-            s.split = k;
+            split = k;
         }
     }
-    s.chunks = s.split * samples;
-    return s;
+    return split;
+}
+
+inline JoinPlan join_plan(int64_t T, int64_t H, int64_t samples, bool fp32)
+{
+    JoinPlan p;
+    static_cast<RowPlan&>(p) = row_plan(H, fp32, true);
+    p.wide = p.vecs * p.width > 16 || p.lanes > kBwdBlock;
+    p.len = samples > 0 ? T / samples : 0;
+    const int32_t least = p.lanes < 64 ? 64 / p.lanes : 1;  // rows of a whole wave
+    int64_t rows = p.wide ? 1 : kBwdBlock / p.lanes;
+    while (rows > least && ((p.len + rows - 1) / rows * samples < kBwdParts || rows > p.len)) rows /= 2;
+    p.rows = int32_t(rows < least ? least : rows);
+    p.block = p.rows * p.lanes;
+    p.groups = (p.len + p.rows - 1) / p.rows;
+    p.split = join_split(p.groups, samples);
+    p.chunks = p.split * samples;
+    p.grid = p.chunks < kBwdParts ? p.chunks : kBwdParts;
+    return p;
 }
 
 hipError_t launch_join_fwd(const JoinArgs& a, int x_dtype, int r_dtype, const RowPlan& p, hipStream_t st);
 
-// The rows' means (a.row) and then the gradients and partial sums, two kernels.
-hipError_t launch_join_bwd_rows(const JoinBwdArgs& a, int x_dtype, int r_dtype, hipStream_t st);
+// The gradients and partial sums in one kernel.
+hipError_t launch_join_bwd(const JoinBwdArgs& a, int x_dtype, int r_dtype, const JoinPlan& p, hipStream_t st);
+// Of wide rows: their means (a.row), then the gradients and partial sums.
+hipError_t launch_join_bwd_wide(const JoinBwdArgs& a, int x_dtype, int r_dtype, hipStream_t st);
 
 // The vectors' gradients from the partial sums.
 struct JoinVecGrads {

@@ -57,6 +57,9 @@ Vec scale_of(const gn_join* j, const void* p)
 {
     return Vec{p, j->scale_stride, j->scale_dtype, j->scale_stride ? j->samples : 1};
 }
+// The means of wide rows.
+size_t means_bytes(int64_t T) { return (size_t(T) * sizeof(float2) + 15) / 16 * 16; }
+
 gn::JoinVec vec(const Vec& v) { return gn::JoinVec{v.p, v.stride, v.dtype}; }
 
 gn::JoinVecs vecs_of(const gn_join* j, const void* w, const void* post, const void* gate, const void* scale)
@@ -169,7 +172,8 @@ int gn::join_backward(const gn_join* j, const JoinBackwardPtrs& p, void* stream,
         return GN_ERR_ALIGN;
     const void *h = reads_h ? p.h : nullptr, *x = reads_x ? p.x : nullptr;
     const int64_t x_stride = ckpt ? H : j->x_stride;
-    const gn::JoinSplit split = gn::join_split(T, samples);
+    const bool fp32 = j->x_dtype == GN_F32 || j->r_dtype == GN_F32;
+    const gn::JoinPlan plan = gn::join_plan(T, H, samples, fp32);
     const Span sdy(p.dy, T * H * xs), sdh(p.dh, T * H * rs), sh(h, T * H * (ckpt ? 1 : rs)),
         sx(x, ckpt ? T * H : rows_bytes(T, H, x_stride, j->x_dtype));
     const Span in[] = {sdy, sdh, sh, sx, Span(h ? p.h_scale : nullptr, T * scales * 4), Span(x ? p.x_scale : nullptr, T * scales * 4),
@@ -197,9 +201,9 @@ int gn::join_backward(const gn_join* j, const JoinBackwardPtrs& p, void* stream,
         return rc;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const gn::JoinVecs v = vecs_of(j, w.p, post.p, gate.p, scale.p);
-    // the rows' means, then the partial sums
-    float2* row = static_cast<float2*>(p.workspace);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + (size_t(T) * sizeof(float2) + 15) / 16 * 16);
+    // the partial sums, behind the rows' means where those are kept
+    char* ws = static_cast<char*>(p.workspace);
+    float* part = reinterpret_cast<float*>(ws + (plan.wide ? means_bytes(T) : 0));
     if (T > 0) {
         gn::JoinBwdArgs a{};
         a.dy = p.dy;
@@ -214,20 +218,28 @@ int gn::join_backward(const gn_join* j, const JoinBackwardPtrs& p, void* stream,
         a.dres = p.dres;
         a.v = v;
         a.part = vectors ? part : nullptr;
-        a.row = row;
+        a.row = plan.wide ? reinterpret_cast<float2*>(ws) : nullptr;
         a.T = T;
         a.H = H;
         a.x_stride = x_stride;
-        a.len = split.len;
-        a.chunks = split.chunks;
-        a.split = split.split;
+        a.len = plan.len;
+        a.groups = plan.groups;
+        a.chunks = plan.chunks;
+        a.split = plan.split;
+        a.lanes = plan.lanes;
+        a.rows = plan.rows;
         a.scales = scales;
         a.inv_H = 1.0f / float(H);
         a.residual_scale = j->residual_scale;
         a.q_dtype = j->q_dtype;
         a.block = int32_t(j->block);
         a.post = j->post_norm != 0;
-        if (hipError_t e = gn::launch_join_bwd_rows(a, j->x_dtype, j->r_dtype, st)) return launch_status(e);
+        const int64_t hs = ckpt ? 1 : rs, xk = ckpt ? 1 : xs;
+        a.nt = T * H * ((p.dy ? xs + hs : 0) + (p.dh ? rs : 0) + (x ? xk : 0) + (p.dx ? xs : 0) + (p.dres ? rs : 0)) >
+               gn::kRowStreamBytes;
+        if (hipError_t e = plan.wide ? gn::launch_join_bwd_wide(a, j->x_dtype, j->r_dtype, st)
+                                     : gn::launch_join_bwd(a, j->x_dtype, j->r_dtype, plan, st))
+            return launch_status(e);
     }
     if (!vectors) return GN_OK;
     gn::JoinVecGrads g{};
@@ -238,8 +250,8 @@ int gn::join_backward(const gn_join* j, const JoinBackwardPtrs& p, void* stream,
     g.dscale = p.dscale;
     g.v = v;
     g.H = H;
-    g.chunks = T > 0 ? split.chunks : 0;
-    g.split = T > 0 ? split.split : 0;
+    g.chunks = T > 0 ? plan.chunks : 0;
+    g.split = T > 0 ? plan.split : 0;
     g.samples = samples;
     return launch_status(gn::launch_join_vectors(g, st));
 }
@@ -298,8 +310,13 @@ int gn_join_forward(const gn_join* j, const void* x, const void* residual, const
 size_t gn_join_workspace_bytes(int64_t T, int64_t H, int64_t samples)
 {
     if (rows_check(T, H, H) || samples < (T ? 1 : 0) || (samples && T % samples)) return 0;
-    const size_t rows = (size_t(T) * sizeof(float2) + 15) / 16 * 16;
-    return std::max<size_t>(rows + size_t(gn::join_split(T, samples).chunks) * size_t(H) * 2 * sizeof(float), 16);
+    // whichever the types will be
+    size_t most = 16;
+    for (const bool fp32 : {false, true}) {
+        const gn::JoinPlan p = gn::join_plan(T, H, samples, fp32);
+        most = std::max(most, (p.wide ? means_bytes(T) : 0) + size_t(p.chunks) * size_t(H) * 2 * sizeof(float));
+    }
+    return most;
 }
 
 int gn_join_backward(const gn_join* j, const void* dy, const void* dh, const void* h, const float* h_scale,

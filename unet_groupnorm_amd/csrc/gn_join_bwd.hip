@@ -1,6 +1,5 @@
-// gn_join_bwd.hip -- backward of the residual join, from its saved tensors or their 8-bit
-// checkpoints: the rows' means, the gradients of both sides and the sums over rows, and the
-// vectors' gradients.
+// gn_join_bwd.hip -- backward of the residual join over rows that fit a workgroup's registers, from
+// its saved tensors or their 8-bit checkpoints.
 //
 //   d    = rstd * (dy * m - xhat * c1) + dh,   c1 = mean(dy * m * xhat)
 //   dres = residual_scale * d,   dx = post_rstd * (d * c - xpost * c2),   c2 = mean(d * c * xpost)
@@ -8,260 +7,269 @@
 //
 // c2 needs d and d needs c1, two reductions one after the other; but d is linear in c1, so
 // c2 = mean((rstd * dy * m + dh) * c * xpost) - rstd * c1 * mean(xhat * c * xpost), and one
-// reduction of three sums gives both.
+// reduction of three sums gives both: one barrier a row.
 #include "gn_join_vec.hpp"
 
 namespace gn {
 
 namespace {
 
-// ------------------------------------------------------------------ two kernels
-
-// Three sums over the `lanes` lanes of a workgroup's row.
-template <int W>
+// Three sums over a row's lanes; with MANY lanes its waves meet in s (three words for each), and the
+// whole workgroup takes part.
+template <bool MANY, int W>
 __device__ __forceinline__ void row_sums(float (&v)[3], const Row<W>& r, uint32_t* s)
 {
-    const int nw = r.lanes >> 6, k = r.lane & 15;
+    if (!MANY) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) v[q] = __uint_as_float(lanes_all<AddOp>(__float_as_uint(v[q]), r.lanes));
+        return;
+    }
+    const int nw = r.lanes >> 6, k = r.lane & 7;  // 8 waves at most
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
         const uint32_t b = lanes_all<AddOp>(__float_as_uint(v[q]), 64);
-        if ((r.lane & 63) == 0) s[q * 16 + (r.lane >> 6)] = b;
+        if ((r.lane & 63) == 0) s[q * nw + (r.lane >> 6)] = b;
     }
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
-        const uint32_t b = s[q * 16 + (k < nw ? k : 0)];
-        v[q] = __uint_as_float(lanes_all<AddOp>(k < nw ? b : 0u, 16));
+        const uint32_t b = s[q * nw + (k < nw ? k : 0)];
+        v[q] = __uint_as_float(lanes_all<AddOp>(k < nw ? b : 0u, 8));
     }
 }
 
-// One piece of a row of everything the backward pass reads, in fp32: zeros in columns that are not
-// the piece's own, and for what is not there.
-template <typename XT, typename HT, bool CK, int W, int END>
-struct JoinPiece {
-    float dy[W], dh[W], h[W], x[W], c[W], m[W];
-    __device__ __forceinline__ void zero(float (&v)[W])
+// A workgroup's walk over the row groups of its chunks.
+struct Walk {
+    int64_t chunk, n, g;  // n: the chunk's sequence, g: the group within it
+    __device__ __forceinline__ void start(const JoinBwdArgs& a, int64_t c)
     {
-#pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = 0.0f;
+        chunk = c;
+        n = c / a.split;
+        g = c - n * a.split;
     }
-    __device__ __forceinline__ void load(const JoinBwdArgs& a, const Row<W>& r, int32_t i, int64_t t, int64_t n)
+    // To the next group; whether that begins another chunk.
+    __device__ __forceinline__ bool step(const JoinBwdArgs& a)
     {
-        Piece<XT, W> rdy;
-        Piece<HT, W> rdh;
-        Saved<HT, W, CK> rh;
-        Saved<XT, W, CK> rx;
-        if (a.dy) load_piece<XT, W, END, false>(in<XT>(a.dy) + t * a.H, r, i, rdy);
-        if (a.dh) load_piece<HT, W, END, false>(in<HT>(a.dh) + t * a.H, r, i, rdh);
-        if (a.dy) rh.template load<END, false>(a.h, t * a.H, r, i, a.h_scale, t * a.scales, a.block);
-        if (a.x) rx.template load<END, false>(a.x, t * a.x_stride, r, i, a.x_scale, t * a.scales, a.block);
-        load_branch<W, END>(a.v, n, r, i, c);
-        load_multiplier<W, END>(a.v, n, r, i, m);
-        zero(dy);
-        zero(dh);
-        zero(h);
-        zero(x);
-        if (a.dy) widen_piece<XT, W, END>(rdy, r, i, dy);
-        if (a.dh) widen_piece<HT, W, END>(rdh, r, i, dh);
-        if (a.dy) rh.template widen<END>(r, i, a.q_dtype, h);
-        if (a.x) rx.template widen<END>(r, i, a.q_dtype, x);
+        g += a.split;
+        if (g < a.groups) return false;
+        start(a, chunk + gridDim.x);
+        return true;
     }
 };
 
-constexpr int kColBlock = 256;
-// Workgroups of a launch of them (the threads of a launch stay below 2^32).
-constexpr int64_t kGroups = int64_t(1) << 23;
-
-// A row's c1 * rstd and c2, one workgroup of 256 threads for each row (of T up to a.T).
-template <typename XT, typename HT, bool CK, int W, int END>
-__global__ void __launch_bounds__(kColBlock)
-join_rows_kernel(JoinBwdArgs a, int64_t first)
+// Workgroup b takes the chunks b, b + gridDim.x, ... (a.rows rows at once, a.lanes lanes each; MANY:
+// more than 64). DEPTH groups' loads are in flight behind the one in use. Every lane keeps its
+// columns' vectors and sums in registers; at a chunk's end the workgroup adds its rows' sums in LDS
+// and leaves two partial sums for each column. FULL: dy, dh, h and x are all there; else each may be
+// missing, behind branches. NT: nontemporal loads.
+template <typename XT, typename HT, bool CK, bool FULL, int W, int V, bool MANY, int END, int DEPTH, bool NT>
+__global__ void __launch_bounds__(kBwdBlock)
+join_bwd_kernel(JoinBwdArgs a)
 {
-    __shared__ uint32_t s[48];
-    const Row<W> r = row_of<W>(a.H, kColBlock, int32_t(threadIdx.x));
-    const int64_t t = first + blockIdx.x, n = sequence_of(t, a.len);
-    const float rstd = a.dy ? a.rstd[t] : 0.0f, post_rstd = a.post ? a.post_rstd[t] : 1.0f;
-    const int32_t pieces = (r.H + W - 1) / W;
-    float v[3] = {0.0f, 0.0f, 0.0f};
-    for (int32_t i = r.lane; i < pieces; i += kColBlock) {
-        JoinPiece<XT, HT, CK, W, END> p;
-        p.load(a, r, i, t, n);
-        float g[W], xh[W], e[W], cx[W];
+    __shared__ uint32_t s_sum[2][3 * (kBwdBlock / 64)];
+    __shared__ __align__(16) float s_part[kBwdBlock * W];
+    int32_t sub = int32_t(threadIdx.x) / a.lanes;
+    if (MANY) sub = __builtin_amdgcn_readfirstlane(sub);
+    const Row<W> r = row_of<W>(a.H, a.lanes, int32_t(threadIdx.x) - sub * a.lanes);
+    struct Loaded {
+        Piece<XT, W> dy[V];
+        Piece<HT, W> dh[V];
+        Saved<HT, W, CK> h[V];
+        Saved<XT, W, CK> x[V];
+        float rstd, post_rstd;
+    };
+    const bool has_dy = FULL || a.dy, has_dh = FULL || a.dh, has_x = FULL || a.x;
+    Walk use, next;
+    use.start(a, blockIdx.x);
+    next = use;
+    const auto row = [&](const Walk& w) { return w.n * a.len + w.g * a.rows + sub; };
+    const auto load = [&](Loaded& l) {
+        // past the last row of the sequence, or of the last chunk: the last row again, unused
+        const int64_t end = next.chunk < a.chunks ? (next.n + 1) * a.len : a.T;
+        int64_t t = row(next);
+        t = t < end ? t : end - 1;
+        const int64_t k = t * a.H, kx = t * a.x_stride, ks = t * a.scales;
 #pragma unroll
-        for (int k = 0; k < W; ++k) {
-            g[k] = p.dy[k] * p.m[k];
-            xh[k] = p.h[k] * rstd;
-            e[k] = fmaf(rstd, g[k], p.dh[k]);
-            cx[k] = p.c[k] * (p.x[k] * post_rstd);
+        for (int u = 0; u < V; ++u) {
+            const int32_t i = r.piece(u);
+            if (has_dy) load_piece<XT, W, END, NT>(in<XT>(a.dy) + k, r, i, l.dy[u]);
+            if (has_dh) load_piece<HT, W, END, NT>(in<HT>(a.dh) + k, r, i, l.dh[u]);
+            if (has_dy) l.h[u].template load<END, NT>(a.h, k, r, i, a.h_scale, ks, a.block);
+            if (has_x) l.x[u].template load<END, NT>(a.x, kx, r, i, a.x_scale, ks, a.block);
         }
-        v[0] = v[0] + tree_sumprod(g, xh);
-        v[1] = v[1] + tree_sumprod(e, cx);
-        v[2] = v[2] + tree_sumprod(xh, cx);
-    }
-    row_sums(v, r, s);
-    const float c1 = v[0] * a.inv_H * rstd;
-    if (threadIdx.x == 0) a.row[t] = float2{c1, fmaf(-c1, v[2], v[1]) * a.inv_H};
-}
-
-// The gradients of a chunk's rows, and its sums: a thread has W columns in registers and walks the
-// rows.
-template <typename XT, typename HT, bool CK, int W, int END>
-__global__ void __launch_bounds__(kColBlock)
-join_cols_kernel(JoinBwdArgs a, int64_t first, uint32_t tiles)
-{
-    const uint32_t k = blockIdx.x / tiles;
-    const int64_t chunk = first + k, n = chunk / a.split;
-    const int32_t i = int32_t(blockIdx.x - k * tiles) * kColBlock + int32_t(threadIdx.x);
-    const Row<W> r = row_of<W>(a.H, kColBlock, int32_t(threadIdx.x));
-    if (i >= (r.H + W - 1) / W) return;
-    float A[W], C[W];
+        l.rstd = has_dy ? a.rstd[t] : 0.0f;
+        l.post_rstd = a.post ? a.post_rstd[t] : 1.0f;
+        next.step(a);
+    };
+    float c[V][W], m[V][W], A[V][W], C[V][W];
+    const auto begin = [&](bool vectors) {  // a chunk
 #pragma unroll
-    for (int e = 0; e < W; ++e) A[e] = C[e] = 0.0f;
-    const int64_t end = (n + 1) * a.len;
-    for (int64_t t = n * a.len + (chunk - n * a.split); t < end; t += a.split) {
-        JoinPiece<XT, HT, CK, W, END> p;
-        p.load(a, r, i, t, n);
-        const float rstd = a.dy ? a.rstd[t] : 0.0f, post_rstd = a.post ? a.post_rstd[t] : 1.0f;
-        const float2 mean = a.row[t];
-        float dres[W], dx[W];
+        for (int u = 0; u < V; ++u) {
+            if (vectors) {
+                load_branch<W, END>(a.v, use.n, r, r.piece(u), c[u]);
+                load_multiplier<W, END>(a.v, use.n, r, r.piece(u), m[u]);
+            }
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            const float xh = p.h[e] * rstd, xp = p.x[e] * post_rstd;
-            float d = fmaf(rstd, p.dy[e] * p.m[e], p.dh[e]);
-            d = a.dy ? fmaf(-xh, mean.x, d) : d;
-            A[e] = fmaf(p.dy[e], xh, A[e]);
-            C[e] = fmaf(d, xp, C[e]);
-            dres[e] = a.residual_scale * d;
-            dx[e] = a.post ? post_rstd * fmaf(-xp, mean.y, d * p.c[e]) : d * p.c[e];
+            for (int e = 0; e < W; ++e) A[u][e] = C[u][e] = 0.0f;
         }
-        if (a.dres) store_values<HT, W, END>(out<HT>(a.dres) + t * a.H, r, i, dres);
-        if (a.dx) store_values<XT, W, END>(out<XT>(a.dx) + t * a.H, r, i, dx);
+    };
+    // A chunk's partial sums of one kind, to part[chunk]. s_part is free after another barrier.
+    const auto leave = [&](float* part, const float (&sum)[V][W]) {
+        part += use.chunk * a.H;
+        if (a.rows == 1) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) store_values<float, W, END>(part, r, r.piece(u), sum[u]);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < W; ++e) s_part[threadIdx.x * W + e] = sum[u][e];
+            __syncthreads();
+            const int32_t first = u * a.lanes * W, n = a.lanes * W;
+            for (int32_t k = threadIdx.x; k < n; k += blockDim.x) {
+                const int32_t i = first / W + k / W, e = k % W;
+                if (END == kTiny ? first + k >= r.H : e < r.skip(i)) continue;
+                float s = s_part[k];
+                for (int32_t j = 1; j < a.rows; ++j) s = s + s_part[j * n + k];
+                part[r.column(i) + e] = s;
+            }
+        }
+    };
+    int phase = 0;
+    const auto group = [&](Loaded& l) {
+        float dy[V][W], x[V][W], h[V][W], e[V][W];
+        const float rstd = l.rstd, post_rstd = l.post_rstd;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int32_t i = r.piece(u);
+#pragma unroll
+            for (int k = 0; k < W; ++k) dy[u][k] = e[u][k] = h[u][k] = x[u][k] = 0.0f;
+            if (has_dy) widen_piece<XT, W, END>(l.dy[u], r, i, dy[u]);
+            if (has_dh) widen_piece<HT, W, END>(l.dh[u], r, i, e[u]);
+            if (has_dy) l.h[u].template widen<END>(r, i, a.q_dtype, h[u]);
+            if (has_x) l.x[u].template widen<END>(r, i, a.q_dtype, x[u]);
+        }
+        load(l);
+        const int64_t t = row(use), at = t * a.H;
+        const bool live = t < (use.n + 1) * a.len;
+        float v[3] = {0.0f, 0.0f, 0.0f};
+        if (live) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                float g[W], cx[W];
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    h[u][k] = h[u][k] * rstd;  // xhat
+                    x[u][k] = x[u][k] * post_rstd;  // xpost
+                    A[u][k] = fmaf(dy[u][k], h[u][k], A[u][k]);
+                    g[k] = dy[u][k] * m[u][k];
+                    e[u][k] = fmaf(rstd, g[k], e[u][k]);
+                    cx[k] = c[u][k] * x[u][k];
+                }
+                v[0] = v[0] + tree_sumprod(g, h[u]);
+                v[1] = v[1] + tree_sumprod(e[u], cx);
+                v[2] = v[2] + tree_sumprod(h[u], cx);
+            }
+        }
+        row_sums<MANY>(v, r, s_sum[phase] + (MANY ? 3 * sub * (r.lanes >> 6) : 0));
+        phase ^= 1;
+        if (live) {  // behind the row's barrier
+            const float c1 = v[0] * a.inv_H * rstd, c2 = fmaf(-c1, v[2], v[1]) * a.inv_H;
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                float o[W];
+                if (has_dy) {
+#pragma unroll
+                    for (int k = 0; k < W; ++k) e[u][k] = fmaf(-h[u][k], c1, e[u][k]);  // d
+                }
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    C[u][k] = fmaf(e[u][k], x[u][k], C[u][k]);
+                    o[k] = a.residual_scale * e[u][k];
+                }
+                if (a.dres) store_values<HT, W, END>(out<HT>(a.dres) + at, r, r.piece(u), o);
+                if (a.post) {
+#pragma unroll
+                    for (int k = 0; k < W; ++k) o[k] = post_rstd * fmaf(-x[u][k], c2, e[u][k] * c[u][k]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < W; ++k) o[k] = e[u][k] * c[u][k];
+                }
+                if (a.dx) store_values<XT, W, END>(out<XT>(a.dx) + at, r, r.piece(u), o);
+            }
+        }
+        const Walk was = use;
+        if (use.step(a)) {
+            if (a.part) {
+                const Walk now = use;
+                use = was;
+                leave(a.part, A);
+                leave(a.part + a.chunks * a.H, C);
+                use = now;
+            }
+            if (use.chunk < a.chunks) begin(use.n != was.n);
+        }
+    };
+    Loaded l[DEPTH];
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k) load(l[k]);
+    begin(true);
+    while (use.chunk < a.chunks) {
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k) {
+            if (k && use.chunk >= a.chunks) break;
+            group(l[k]);
+        }
     }
-    if (!a.part) return;
-    store_values<float, W, END>(a.part + chunk * a.H, r, i, A);
-    store_values<float, W, END>(a.part + (a.chunks + chunk) * a.H, r, i, C);
 }
 
 template <typename XT, typename HT, int W, bool CK>
-hipError_t two(const JoinBwdArgs& a, hipStream_t st)
+hipError_t one(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st)
 {
-    const auto go = [&](auto end) {
-        constexpr int E = decltype(end)::value;
-        for (int64_t t = 0; t < a.T; t += kGroups)
-            if (hipError_t e = launch(join_rows_kernel<XT, HT, CK, W, E>,
-                                      dim3(unsigned(a.T - t < kGroups ? a.T - t : kGroups)), dim3(kColBlock), st, a, t))
-                return e;
-        const int64_t tiles = ((a.H + W - 1) / W + kColBlock - 1) / kColBlock, most = kGroups / tiles;
-        for (int64_t k = 0; k < a.chunks; k += most)
-            if (hipError_t e = launch(join_cols_kernel<XT, HT, CK, W, E>,
-                                      dim3(unsigned(tiles * (a.chunks - k < most ? a.chunks - k : most))), dim3(kColBlock),
-                                      st, a, k, uint32_t(tiles)))
-                return e;
-        return hipSuccess;
+    const dim3 grid = dim3(unsigned(p.grid)), block = dim3(p.block);
+    const bool full = a.dy && a.dh && a.x;
+    const auto go = [&](auto v, auto end) {
+        constexpr int V = decltype(v)::value, E = decltype(end)::value, kDepth = V * W <= 8 ? 2 : 1;
+        const auto with = [&](auto many) {
+            constexpr bool M = decltype(many)::value;
+            if (!full) return launch(join_bwd_kernel<XT, HT, CK, false, W, V, M, E == kTiny ? kTiny : kEnds, 1, false>, grid, block, st, a);
+            if constexpr (E == kExact)
+                if (a.nt) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, true>, grid, block, st, a);
+            return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, false>, grid, block, st, a);
+        };
+        if constexpr (V == 1)
+            if (p.lanes <= 64) return with(std::false_type{});
+        if constexpr (E == kTiny)
+            return hipErrorInvalidValue;  // one lane, above
+        else
+            return with(std::true_type{});
     };
-    return a.H < W ? go(std::integral_constant<int, kTiny>{}) : go(std::integral_constant<int, kEnds>{});
+    using Exact = std::integral_constant<int, kExact>;
+    using Ends = std::integral_constant<int, kEnds>;
+    if (a.H < W) return go(std::integral_constant<int, 1>{}, std::integral_constant<int, kTiny>{});
+    const auto pieces = [&](auto v) { return p.exact ? go(v, Exact{}) : go(v, Ends{}); };
+    if (p.vecs == 1) return pieces(std::integral_constant<int, 1>{});
+    if (p.vecs == 2) return pieces(std::integral_constant<int, 2>{});
+    if constexpr (W == 4)
+        if (p.vecs == 4) return pieces(std::integral_constant<int, 4>{});
+    return hipErrorInvalidValue;
 }
 
 template <typename XT, typename HT, int W>
-hipError_t two(const JoinBwdArgs& a, hipStream_t st)
+hipError_t one(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st)
 {
-    return a.h_scale || a.x_scale ? two<XT, HT, W, true>(a, st) : two<XT, HT, W, false>(a, st);
-}
-
-// ------------------------------------------------------------------ the vectors' gradients
-
-constexpr int kVecBlock = 1024, kVecCols = 32, kVecSlices = kVecBlock / (kVecCols / 4);
-
-__device__ __forceinline__ float vector_at(const JoinVec& v, int64_t n, int64_t c, float none)
-{
-    if (!v.p) return none;
-    const int64_t k = n * v.stride + c;
-    return v.dtype == GN_F32 ? in<float>(v.p)[k] : v.dtype == GN_BF16 ? Io<uint16_t>::load1(in<uint16_t>(v.p) + k)
-                                                                      : Io<_Float16>::load1(in<_Float16>(v.p) + k);
-}
-
-__device__ __forceinline__ void store_as(void* p, int dtype, int64_t k, float x)
-{
-    if (dtype == GN_F32)
-        Io<float>::store1(out<float>(p) + k, x);
-    else if (dtype == GN_BF16)
-        Io<uint16_t>::store1(out<uint16_t>(p) + k, x);
-    else
-        Io<_Float16>::store1(out<_Float16>(p) + k, x);
-}
-
-// A workgroup adds 32 columns of the partial sums, a thread 4 columns of the chunks slice, slice +
-// 128, ...: workgroup row 0 of all sequences, row 1 + n of sequence n (where the gate or the scale
-// is a vector for each).
-__global__ void __launch_bounds__(kVecBlock)
-join_vectors_kernel(JoinVecGrads a, int64_t first, uint32_t tiles)
-{
-    __shared__ float s[4][kVecSlices][kVecCols + 1];
-    const uint32_t part_row = blockIdx.x / tiles;
-    const int64_t row = first + part_row;
-    const int64_t col0 = int64_t(blockIdx.x - part_row * tiles) * kVecCols;
-    const bool all = row == 0;
-    const int quad = threadIdx.x & 7, slice = threadIdx.x >> 3;
-    const int64_t from = all ? 0 : (row - 1) * a.split, to = all ? a.chunks : from + a.split;
-    float v[4][4];  // A, C, A * (1 + scale), C * gate
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[q][e] = 0.0f;
-    for (int64_t p = from + slice; p < to; p += kVecSlices) {
-        const int64_t n = p / a.split;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t c = col0 + quad * 4 + e;
-            if (c >= a.H) continue;
-            const float A = a.part[p * a.H + c], C = a.part[(a.chunks + p) * a.H + c];
-            v[0][e] = v[0][e] + A;
-            v[1][e] = v[1][e] + C;
-            if (all) {
-                v[2][e] = fmaf(1.0f + vector_at(a.v.scale, n, c, 0.0f), A, v[2][e]);
-                v[3][e] = fmaf(a.v.branch_scale * vector_at(a.v.gate, n, c, 1.0f), C, v[3][e]);
-            }
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[q][slice][quad * 4 + e] = v[q][e];
-    __syncthreads();
-    const int q = threadIdx.x >> 5, c = threadIdx.x & 31;
-    if (q >= 4 || col0 + c >= a.H) return;
-    float x = 0.0f;
-    for (int k = 0; k < kVecSlices; ++k) x = x + s[q][k][c];
-    const int64_t col = col0 + c;
-    const bool mine_gate = all == (a.v.gate.stride == 0), mine_scale = all == (a.v.scale.stride == 0);
-    const int64_t n = all ? 0 : row - 1;
-    if (q == 0 && a.dscale && mine_scale)
-        store_as(a.dscale, a.v.scale.dtype, n * a.H + col, vector_at(a.v.w, 0, col, 1.0f) * x);
-    if (q == 1 && a.dgate && mine_gate)
-        store_as(a.dgate, a.v.gate.dtype, n * a.H + col, a.v.branch_scale * vector_at(a.v.post, 0, col, 1.0f) * x);
-    if (q == 2 && a.dw && all) store_as(a.dw, a.v.w.dtype, col, x);
-    if (q == 3 && a.dpost && all) store_as(a.dpost, a.v.post.dtype, col, x);
+    return a.h_scale || a.x_scale ? one<XT, HT, W, true>(a, p, st) : one<XT, HT, W, false>(a, p, st);
 }
 
 }  // namespace
 
-hipError_t launch_join_bwd_rows(const JoinBwdArgs& a, int x_dtype, int r_dtype, hipStream_t st)
+hipError_t launch_join_bwd(const JoinBwdArgs& a, int x_dtype, int r_dtype, const JoinPlan& p, hipStream_t st)
 {
-    if (x_dtype == GN_F32) return two<float, float, 4>(a, st);
-    if (r_dtype == GN_F32) return x_dtype == GN_BF16 ? two<uint16_t, float, 4>(a, st) : two<_Float16, float, 4>(a, st);
-    return x_dtype == GN_BF16 ? two<uint16_t, uint16_t, 8>(a, st) : two<_Float16, _Float16, 8>(a, st);
-}
-
-hipError_t launch_join_vectors(const JoinVecGrads& a, hipStream_t st)
-{
-    const int64_t tiles = (a.H + kVecCols - 1) / kVecCols;
-    const bool each = (a.dgate && a.v.gate.stride) || (a.dscale && a.v.scale.stride);
-    const int64_t rows = 1 + (each ? a.samples : 0), most = (int64_t(1) << 21) / tiles;
-    for (int64_t k = 0; k < rows; k += most)
-        if (hipError_t e = launch(join_vectors_kernel, dim3(unsigned(tiles * (rows - k < most ? rows - k : most))),
-                                  dim3(kVecBlock), st, a, k, uint32_t(tiles)))
-            return e;
-    return hipSuccess;
+    if (x_dtype == GN_F32) return one<float, float, 4>(a, p, st);
+    if (r_dtype == GN_F32) return x_dtype == GN_BF16 ? one<uint16_t, float, 4>(a, p, st) : one<_Float16, float, 4>(a, p, st);
+    return x_dtype == GN_BF16 ? one<uint16_t, uint16_t, 8>(a, p, st) : one<_Float16, _Float16, 8>(a, p, st);
 }
 
 }  // namespace gn
