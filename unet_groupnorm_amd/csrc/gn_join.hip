@@ -80,17 +80,15 @@ join_fwd_kernel(JoinArgs a)
     const int64_t t = int64_t(blockIdx.x) * a.rows + sub;
     if (t >= a.T) return;  // whole rows leave, and with more than 64 lanes whole workgroups
     const bool many = V > 1 || a.lanes > 64;
-    float x[V][W], h[V][W], c[V][W], m[V][W];
+    float x[V][W], h[V][W];
     Piece<XT, W> rx[V];
     Piece<HT, W> rr[V];
     load_row<XT, W, V, END>(in<XT>(a.x) + t * a.x_stride, r, a.nt, rx);
     load_row<HT, W, V, END>(in<HT>(a.res) + t * a.H, r, a.nt, rr);
     const int64_t n = a.one ? 0 : sequence_of(a.first + t, a.len);
+    RawVecs<W> rv[V];
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-        load_branch<W, END>(a.v, n, r, r.piece(u), c[u]);
-        if (a.y) load_multiplier<W, END>(a.v, n, r, r.piece(u), m[u]);
-    }
+    for (int u = 0; u < V; ++u) rv[u].template load<END>(a.v, n, r, r.piece(u));
     float ss = 0.0f;
     uint32_t top = 0;
 #pragma unroll
@@ -113,9 +111,11 @@ join_fwd_kernel(JoinArgs a)
     ss = 0.0f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
+        float c[W];
+        rv[u].template branch<END>(a.v, r, r.piece(u), c);
         widen_piece<HT, W, END>(rr[u], r, r.piece(u), h[u]);
 #pragma unroll
-        for (int e = 0; e < W; ++e) h[u][e] = fmaf(x[u][e] * post_rstd, c[u][e], a.residual_scale * h[u][e]);
+        for (int e = 0; e < W; ++e) h[u][e] = fmaf(x[u][e] * post_rstd, c[e], a.residual_scale * h[u][e]);
         rr[u].narrow(h[u]);  // taken as stored
         rr[u].widen(h[u]);
         if (END == kEnds && r.piece(u) >= r.full) {  // columns that are not its own: 0 * inf is NaN
@@ -136,8 +136,10 @@ join_fwd_kernel(JoinArgs a)
     if (a.rstd && r.lane == 0) a.rstd[t] = rstd;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
+        float m[W];
+        rv[u].template multiplier<END>(a.v, r, r.piece(u), m);
 #pragma unroll
-        for (int e = 0; e < W; ++e) h[u][e] = h[u][e] * rstd * m[u][e];
+        for (int e = 0; e < W; ++e) h[u][e] = h[u][e] * rstd * m[e];
         store_values<XT, W, END>(out<XT>(a.y) + t * a.H, r, r.piece(u), h[u]);
     }
 }

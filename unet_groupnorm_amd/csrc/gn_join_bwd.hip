@@ -102,16 +102,21 @@ join_bwd_kernel(JoinBwdArgs a)
         next.step(a);
     };
     float c[V][W], m[V][W], A[V][W], C[V][W];
-    const auto begin = [&](bool vectors) {  // a chunk
+    const auto vectors = [&]() {  // of a sequence
+        RawVecs<W> rv[V];
+#pragma unroll
+        for (int u = 0; u < V; ++u) rv[u].template load<END>(a.v, use.n, r, r.piece(u));
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            if (vectors) {
-                load_branch<W, END>(a.v, use.n, r, r.piece(u), c[u]);
-                load_multiplier<W, END>(a.v, use.n, r, r.piece(u), m[u]);
-            }
+            rv[u].template branch<END>(a.v, r, r.piece(u), c[u]);
+            rv[u].template multiplier<END>(a.v, r, r.piece(u), m[u]);
+        }
+    };
+    const auto zero = [&]() {
+#pragma unroll
+        for (int u = 0; u < V; ++u)
 #pragma unroll
             for (int e = 0; e < W; ++e) A[u][e] = C[u][e] = 0.0f;
-        }
     };
     // A chunk's partial sums of one kind, to part[chunk]. s_part is free after another barrier.
     const auto leave = [&](float* part, const float (&sum)[V][W]) {
@@ -209,13 +214,15 @@ join_bwd_kernel(JoinBwdArgs a)
                 leave(a.part + a.chunks * a.H, C);
                 use = now;
             }
-            if (use.chunk < a.chunks) begin(use.n != was.n);
+            zero();
+            if (use.chunk < a.chunks && use.n != was.n) vectors();
         }
     };
+    vectors();  // first: behind rows in flight they would wait for those
+    zero();
     Loaded l[DEPTH];
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) load(l[k]);
-    begin(true);
     while (use.chunk < a.chunks) {
 #pragma unroll
         for (int k = 0; k < DEPTH; ++k) {

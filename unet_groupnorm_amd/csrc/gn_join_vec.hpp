@@ -16,29 +16,101 @@ __device__ __forceinline__ const void* vector_of(const JoinVec& v, int64_t n)
     return !v.p ? nullptr : v.dtype == GN_F32 ? static_cast<const void*>(in<float>(v.p) + e) : in<uint16_t>(v.p) + e;
 }
 
-// Piece i of the coefficient c = (branch_scale * gate) * post_weight of sequence n.
-template <int W, int END>
-__device__ __forceinline__ void load_branch(const JoinVecs& j, int64_t n, const Row<W>& r, int32_t i, float (&c)[W])
-{
-    float p[W];
-    load_weight<W, END>(vector_of(j.gate, n), j.gate.dtype, r, i, c);
-    load_weight<W, END>(j.post.p, j.post.dtype, r, i, p);
+// A piece of a vector as loaded, of whatever type: the load by itself, so that the four vectors' loads
+// are in flight together (one after the other each waits for the one before).
+template <int W>
+struct RawVec {
+    uint32_t w[W];  // fp32 in all of them, 16-bit types in the first half
+    template <int END>
+    __device__ __forceinline__ void load(const void* p, int dtype, const Row<W>& r, int32_t i)
+    {
+        if (!p) return;
+        if (END == kTiny) {  // as fp32
+            float v[W];
+            load_weight<W, END>(p, dtype, r, i, v);
 #pragma unroll
-    for (int e = 0; e < W; ++e) c[e] = j.branch_scale * c[e] * p[e];
-}
+            for (int e = 0; e < W; ++e) w[e] = __float_as_uint(v[e]);
+            return;
+        }
+        const int32_t c = END == kExact ? i * W : r.column(i);
+        if (dtype == GN_F32) {
+#pragma unroll
+            for (int k = 0; k < W; k += 4) {
+                Piece<float, 4> q;
+                q.load<false>(in<float>(p) + c + k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[k + e] = q.w[e];
+            }
+        } else {
+            Piece<uint16_t, W> q;
+            q.template load<false>(in<uint16_t>(p) + c);
+#pragma unroll
+            for (int e = 0; e < W / 2; ++e) w[e] = q.w[e];
+        }
+    }
+    // Its values, `none` where there is no vector, zeros in columns that are not the piece's own.
+    template <int END>
+    __device__ __forceinline__ void widen(const void* p, int dtype, const Row<W>& r, int32_t i, float none,
+                                          float (&v)[W]) const
+    {
+        if (!p) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = none;
+            return;
+        }
+        if (END == kTiny || dtype == GN_F32) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = __uint_as_float(w[e]);
+        } else {
+            Piece<uint16_t, W> q;
+#pragma unroll
+            for (int e = 0; e < W / 2; ++e) q.w[e] = w[e];
+            if (dtype == GN_BF16)
+                q.widen(v);
+            else
+                Piece<_Float16, W>{q.w}.widen(v);
+        }
+        if (END == kEnds && i >= r.full) {
+            const int32_t skip = r.skip(i);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[e] = e < skip ? 0.0f : v[e];
+        }
+    }
+};
 
-// Piece i of the multiplier m = weight * (1 + scale) of sequence n.
-template <int W, int END>
-__device__ __forceinline__ void load_multiplier(const JoinVecs& j, int64_t n, const Row<W>& r, int32_t i, float (&m)[W])
-{
-    load_weight<W, END>(j.w.p, j.w.dtype, r, i, m);
-    if (j.scale.p) {
+// A piece of the four vectors of sequence n.
+template <int W>
+struct RawVecs {
+    RawVec<W> gate, post, w, scale;
+    template <int END>
+    __device__ __forceinline__ void load(const JoinVecs& j, int64_t n, const Row<W>& r, int32_t i)
+    {
+        gate.template load<END>(vector_of(j.gate, n), j.gate.dtype, r, i);
+        post.template load<END>(j.post.p, j.post.dtype, r, i);
+        w.template load<END>(j.w.p, j.w.dtype, r, i);
+        scale.template load<END>(vector_of(j.scale, n), j.scale.dtype, r, i);
+    }
+    // The coefficient c = (branch_scale * gate) * post_weight.
+    template <int END>
+    __device__ __forceinline__ void branch(const JoinVecs& j, const Row<W>& r, int32_t i, float (&c)[W]) const
+    {
+        float p[W];
+        gate.template widen<END>(j.gate.p, j.gate.dtype, r, i, 1.0f, c);
+        post.template widen<END>(j.post.p, j.post.dtype, r, i, 1.0f, p);
+#pragma unroll
+        for (int e = 0; e < W; ++e) c[e] = j.branch_scale * c[e] * p[e];
+    }
+    // The multiplier m = weight * (1 + scale).
+    template <int END>
+    __device__ __forceinline__ void multiplier(const JoinVecs& j, const Row<W>& r, int32_t i, float (&m)[W]) const
+    {
         float s[W];
-        load_weight<W, END>(vector_of(j.scale, n), j.scale.dtype, r, i, s);
+        w.template widen<END>(j.w.p, j.w.dtype, r, i, 1.0f, m);
+        scale.template widen<END>(j.scale.p, j.scale.dtype, r, i, 0.0f, s);
 #pragma unroll
         for (int e = 0; e < W; ++e) m[e] = m[e] * (1.0f + s[e]);
     }
-}
+};
 
 // The sequence of row t.
 __device__ __forceinline__ int64_t sequence_of(int64_t t, int64_t len)

@@ -47,8 +47,10 @@ struct JoinPiece {
         if (a.dh) load_piece<HT, W, END, false>(in<HT>(a.dh) + t * a.H, r, i, rdh);
         if (a.dy) rh.template load<END, false>(a.h, t * a.H, r, i, a.h_scale, t * a.scales, a.block);
         if (a.x) rx.template load<END, false>(a.x, t * a.x_stride, r, i, a.x_scale, t * a.scales, a.block);
-        load_branch<W, END>(a.v, n, r, i, c);
-        load_multiplier<W, END>(a.v, n, r, i, m);
+        RawVecs<W> rv;
+        rv.template load<END>(a.v, n, r, i);
+        rv.template branch<END>(a.v, r, i, c);
+        rv.template multiplier<END>(a.v, r, i, m);
         zero(dy);
         zero(dh);
         zero(h);
@@ -164,12 +166,34 @@ hipError_t two(const JoinBwdArgs& a, hipStream_t st)
 
 constexpr int kVecBlock = 1024, kVecCols = 32, kVecSlices = kVecBlock / (kVecCols / 4);
 
-__device__ __forceinline__ float vector_at(const JoinVec& v, int64_t n, int64_t c, float none)
+// Columns c to c + 3 of v's vector of sequence n (those below H), `none` where there is none.
+__device__ __forceinline__ void vector4(const JoinVec& v, int64_t n, int64_t c, int64_t H, float none, float (&x)[4])
 {
-    if (!v.p) return none;
-    const int64_t k = n * v.stride + c;
-    return v.dtype == GN_F32 ? in<float>(v.p)[k] : v.dtype == GN_BF16 ? Io<uint16_t>::load1(in<uint16_t>(v.p) + k)
-                                                                      : Io<_Float16>::load1(in<_Float16>(v.p) + k);
+    const void* p = vector_of(v, n);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = none;
+    if (!p) return;
+    const auto take = [&](auto t) {
+        using T = decltype(t);
+        Piece<T, 4> q;
+        if (H - c >= 4)
+            q.template load<false>(in<T>(p) + c);
+        else
+            q.load_part(in<T>(p) + c, H > c ? int(H - c) : 0);
+        q.widen(x);
+    };
+    if (v.dtype == GN_F32)
+        take(float{});
+    else if (v.dtype == GN_BF16)
+        take(uint16_t{});
+    else
+        take(_Float16{});
+}
+
+__device__ __forceinline__ float vector_at(const JoinVec& v, int64_t c, float none)
+{
+    return !v.p ? none : v.dtype == GN_F32 ? in<float>(v.p)[c] : v.dtype == GN_BF16 ? Io<uint16_t>::load1(in<uint16_t>(v.p) + c)
+                                                                                  : Io<_Float16>::load1(in<_Float16>(v.p) + c);
 }
 
 __device__ __forceinline__ void store_as(void* p, int dtype, int64_t k, float x)
@@ -182,57 +206,105 @@ __device__ __forceinline__ void store_as(void* p, int dtype, int64_t k, float x)
         Io<_Float16>::store1(out<_Float16>(p) + k, x);
 }
 
-// A workgroup adds 32 columns of the partial sums, a thread 4 columns of the chunks slice, slice +
-// 128, ...: workgroup row 0 of all sequences, row 1 + n of sequence n (where the gate or the scale
-// is a vector for each).
+// Columns c to c + 3 of chunk p's partial sums of A and C.
+__device__ __forceinline__ void partials4(const JoinVecGrads& a, int64_t p, int64_t c, float (&A)[4], float (&C)[4])
+{
+    Piece<float, 4> qa, qc;
+    const float *pa = a.part + p * a.H + c, *pc = pa + a.chunks * a.H;
+    if (a.H - c >= 4) {
+        qa.load<false>(pa);
+        qc.load<false>(pc);
+    } else {
+        const int n = a.H > c ? int(a.H - c) : 0;
+        qa.load_part(pa, n);
+        qc.load_part(pc, n);
+    }
+    qa.widen(A);
+    qc.widen(C);
+}
+
+// A workgroup adds 32 columns of the partial sums, a thread 4 columns. The first `tiles` workgroups
+// add all sequences' chunks, a thread those at slice, slice + 128, ...; the others take `per`
+// sequences each (where the gate or the scale is a vector for each), a thread the chunks at its place
+// within one. Bound by trips to memory, not by bytes. Sums of A and of C, and weighted by the
+// sequences' vectors where those differ.
 __global__ void __launch_bounds__(kVecBlock)
-join_vectors_kernel(JoinVecGrads a, int64_t first, uint32_t tiles)
+join_vectors_kernel(JoinVecGrads a, int64_t first, uint32_t tiles, int32_t per)
 {
     __shared__ float s[4][kVecSlices][kVecCols + 1];
-    const uint32_t part_row = blockIdx.x / tiles;
-    const int64_t row = first + part_row;
-    const int64_t col0 = int64_t(blockIdx.x - part_row * tiles) * kVecCols;
-    const bool all = row == 0;
+    const uint32_t turn = blockIdx.x / tiles;
+    const int64_t row = first + turn;
+    const int64_t col0 = int64_t(blockIdx.x - turn * tiles) * kVecCols;
     const int quad = threadIdx.x & 7, slice = threadIdx.x >> 3;
-    const int64_t from = all ? 0 : (row - 1) * a.split, to = all ? a.chunks : from + a.split;
+    const int64_t c0 = col0 + quad * 4;
+    const bool all = row == 0, gates = a.v.gate.stride != 0, scales = a.v.scale.stride != 0;
+    const int lanes = all ? kVecSlices : kVecSlices / per;  // of a sum
+    const int64_t n = all ? 0 : (row - 1) * per + slice / lanes;
+    const int64_t from = n * a.split, to = all ? a.chunks : n < a.samples ? from + a.split : from;
     float v[4][4];  // A, C, A * (1 + scale), C * gate
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[q][e] = 0.0f;
-    for (int64_t p = from + slice; p < to; p += kVecSlices) {
-        const int64_t n = p / a.split;
+#pragma unroll 2
+    for (int64_t p = from + (slice & (lanes - 1)); p < to; p += lanes) {
+        float A[4], C[4], w[4];
+        partials4(a, p, c0, A, C);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int64_t c = col0 + quad * 4 + e;
-            if (c >= a.H) continue;
-            const float A = a.part[p * a.H + c], C = a.part[(a.chunks + p) * a.H + c];
-            v[0][e] = v[0][e] + A;
-            v[1][e] = v[1][e] + C;
-            if (all) {
-                v[2][e] = fmaf(1.0f + vector_at(a.v.scale, n, c, 0.0f), A, v[2][e]);
-                v[3][e] = fmaf(a.v.branch_scale * vector_at(a.v.gate, n, c, 1.0f), C, v[3][e]);
+            v[0][e] = v[0][e] + A[e];
+            v[1][e] = v[1][e] + C[e];
+        }
+        if (all && scales) {
+            vector4(a.v.scale, sequence_of(p, a.split), c0, a.H, 0.0f, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[2][e] = fmaf(1.0f + w[e], A[e], v[2][e]);
+        }
+        if (all && gates) {
+            vector4(a.v.gate, sequence_of(p, a.split), c0, a.H, 1.0f, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[3][e] = fmaf(a.v.branch_scale * w[e], C[e], v[3][e]);
+        }
+    }
+    if (all) {  // lanes 8, 16 and 32 apart hold the wave's other slices
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if ((q == 2 && !scales) || (q == 3 && !gates)) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t b = __float_as_uint(v[q][e]);
+                b = AddOp::f(b, dpp<0x128>(b));
+                const auto x = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+                b = AddOp::f(x[0], x[1]);
+                const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+                v[q][e] = __uint_as_float(AddOp::f(y[0], y[1]));
             }
         }
     }
+    if (!all || (threadIdx.x & 63) < 8)
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[q][slice][quad * 4 + e] = v[q][e];
+            for (int e = 0; e < 4; ++e) s[q][all ? threadIdx.x >> 6 : slice][quad * 4 + e] = v[q][e];
     __syncthreads();
-    const int q = threadIdx.x >> 5, c = threadIdx.x & 31;
-    if (q >= 4 || col0 + c >= a.H) return;
-    float x = 0.0f;
-    for (int k = 0; k < kVecSlices; ++k) x = x + s[q][k][c];
-    const int64_t col = col0 + c;
-    const bool mine_gate = all == (a.v.gate.stride == 0), mine_scale = all == (a.v.scale.stride == 0);
-    const int64_t n = all ? 0 : row - 1;
-    if (q == 0 && a.dscale && mine_scale)
-        store_as(a.dscale, a.v.scale.dtype, n * a.H + col, vector_at(a.v.w, 0, col, 1.0f) * x);
-    if (q == 1 && a.dgate && mine_gate)
-        store_as(a.dgate, a.v.gate.dtype, n * a.H + col, a.v.branch_scale * vector_at(a.v.post, 0, col, 1.0f) * x);
-    if (q == 2 && a.dw && all) store_as(a.dw, a.v.w.dtype, col, x);
-    if (q == 3 && a.dpost && all) store_as(a.dpost, a.v.post.dtype, col, x);
+    const int terms = all ? kVecBlock / 64 : lanes;
+    // a thread for each kind of sum, sequence and column
+    const int sums = (all ? 4 : 2 * per) * kVecCols;
+    for (int k = threadIdx.x; k < sums; k += kVecBlock) {
+        const int c = k & (kVecCols - 1), q = all ? k / kVecCols : k / (kVecCols * per), j = all ? 0 : k / kVecCols - q * per;
+        const int64_t col = col0 + c, m = all ? 0 : (row - 1) * per + j;
+        if (col >= a.H || (!all && m >= a.samples)) continue;
+        const int of = q == 2 && !scales ? 0 : q == 3 && !gates ? 1 : q;
+        float x = 0.0f;
+        for (int i = 0; i < terms; ++i) x = x + s[of][j * terms + i][c];
+        if (q == 0 && a.dscale && all == !scales)
+            store_as(a.dscale, a.v.scale.dtype, m * a.H + col, vector_at(a.v.w, col, 1.0f) * x);
+        if (q == 1 && a.dgate && all == !gates)
+            store_as(a.dgate, a.v.gate.dtype, m * a.H + col, a.v.branch_scale * vector_at(a.v.post, col, 1.0f) * x);
+        if (q == 2 && a.dw) store_as(a.dw, a.v.w.dtype, col, scales ? x : (1.0f + vector_at(a.v.scale, col, 0.0f)) * x);
+        if (q == 3 && a.dpost)
+            store_as(a.dpost, a.v.post.dtype, col, gates ? x : a.v.branch_scale * vector_at(a.v.gate, col, 1.0f) * x);
+    }
 }
 
 }  // namespace
@@ -248,10 +320,12 @@ hipError_t launch_join_vectors(const JoinVecGrads& a, hipStream_t st)
 {
     const int64_t tiles = (a.H + kVecCols - 1) / kVecCols;
     const bool each = (a.dgate && a.v.gate.stride) || (a.dscale && a.v.scale.stride);
-    const int64_t rows = 1 + (each ? a.samples : 0), most = (int64_t(1) << 21) / tiles;
+    int32_t per = kVecSlices;  // sequences of a workgroup: as many as its slices have room for
+    while (per > 1 && kVecSlices / per < a.split) per /= 2;
+    const int64_t rows = 1 + (each ? (a.samples + per - 1) / per : 0), most = (int64_t(1) << 21) / tiles;
     for (int64_t k = 0; k < rows; k += most)
         if (hipError_t e = launch(join_vectors_kernel, dim3(unsigned(tiles * (rows - k < most ? rows - k : most))),
-                                  dim3(kVecBlock), st, a, k, uint32_t(tiles)))
+                                  dim3(kVecBlock), st, a, k, uint32_t(tiles), per))
             return e;
     return hipSuccess;
 }
