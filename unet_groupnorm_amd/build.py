@@ -6,7 +6,7 @@ libgn.so: the C ABI (csrc/gn_api.cpp), the launch plans (csrc/gn_plan.cpp) and t
 csrc/gn_kernels_shard.hip for spatial shards), and beside them the row norm and the
 gradient list (csrc/gn_ops_api.cpp, csrc/gn_rms.hip, csrc/gn_rms_bwd.hip,
 csrc/gn_grad.hip), the residual join and the 8-bit checkpoints (csrc/gn_join_api.cpp,
-csrc/gn_join.hip, csrc/gn_join_bwd.hip, csrc/gn_join_wide.hip); compiled with hipcc one source at a time in parallel, then linked into ``unet_groupnorm_amd/libgn.so``.
+csrc/gn_join.hip, csrc/gn_join_wide.hip, csrc/gn_join_bwd_*.hip); compiled with hipcc one source at a time in parallel, then linked into ``unet_groupnorm_amd/libgn.so``.
 
 _gnbind (csrc/gn_binding.cpp, csrc/gn_ops_binding.cpp and csrc/gn_join_binding.cpp, a Python
 extension module linked against libgn.so and torch): the compiled marshalling of the per-step
@@ -33,7 +33,8 @@ PROBE_LIB = os.path.join(HERE, "libgn_probe.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["gn_plan.cpp", "gn_api.cpp", "gn_kernels.hip", "gn_kernels_cl.hip", "gn_kernels_shard.hip",
            "gn_ops_api.cpp", "gn_rms.hip", "gn_rms_bwd.hip", "gn_grad.hip",
-           "gn_join_api.cpp", "gn_join.hip", "gn_join_bwd.hip", "gn_join_wide.hip"]
+           "gn_join_api.cpp", "gn_join.hip", "gn_join_wide.hip", "gn_join_bwd_16.hip", "gn_join_bwd_mixed.hip",
+           "gn_join_bwd_f32.hip"]
 PROBE_SOURCES = ["probe_kernels.hip"]
 BIND_SOURCES = ["gn_binding.cpp", "gn_ops_binding.cpp", "gn_join_binding.cpp"]
 BIND_NAME = "_gnbind"

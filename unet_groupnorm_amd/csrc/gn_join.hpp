@@ -1,5 +1,5 @@
 // gn_join.hpp -- kernel arguments, plans and launchers shared by gn_join_api.cpp and the kernel
-// files of the residual join (gn_join.hip, gn_join_bwd.hip, gn_join_wide.hip) and of the 8-bit
+// files of the residual join (gn_join.hip, gn_join_bwd.hpp, gn_join_wide.hip) and of the 8-bit
 // checkpoints (gn_join.hip).
 #pragma once
 
@@ -76,6 +76,7 @@ struct JoinBwdArgs {
 // chunks, chunk k taking the groups k, k + split, ... of its sequence; a workgroup takes whole
 // chunks and leaves two partial sums for each column of each. Rows of more than 16 columns a lane do
 // not fit (wide): they take two kernels, a thread of the second a few columns of a chunk.
+constexpr int64_t kJoinParts = 256;
 struct JoinPlan : RowPlan {
     int64_t len, groups;     // rows and groups of a sequence
     int64_t split, chunks;   // chunks of a sequence, of all
@@ -83,19 +84,19 @@ struct JoinPlan : RowPlan {
     bool wide;
 };
 
-// The chunks of a sequence of `groups` groups: as many as fill the chip's kBwdParts workgroups in
+// The chunks of a sequence of `groups` groups: as many as fill the chip's kJoinParts workgroups in
 // whole turns as well as up to eight turns can.
 inline int64_t join_split(int64_t groups, int64_t samples)
 {
-    if (groups < 2 || samples >= 8 * kBwdParts) return 1;
+    if (groups < 2 || samples >= 8 * kJoinParts) return 1;
     int64_t split = 1;
     double best = -1.0;
     for (int64_t turns = 1; turns <= 8; ++turns) {
-        int64_t k = turns * kBwdParts / samples;
+        int64_t k = turns * kJoinParts / samples;
         if (k < 1) continue;
         k = k < groups ? k : groups;
-        const int64_t chunks = k * samples, rounds = (chunks + kBwdParts - 1) / kBwdParts;
-        const double used = double(chunks) / double(rounds * kBwdParts);
+        const int64_t chunks = k * samples, rounds = (chunks + kJoinParts - 1) / kJoinParts;
+        const double used = double(chunks) / double(rounds * kJoinParts);
         if (used > best + 0.03) {
             best = used;
             split = k;
@@ -112,20 +113,28 @@ inline JoinPlan join_plan(int64_t T, int64_t H, int64_t samples, bool fp32)
     p.len = samples > 0 ? T / samples : 0;
     const int32_t least = p.lanes < 64 ? 64 / p.lanes : 1;  // rows of a whole wave
     int64_t rows = p.wide ? 1 : kBwdBlock / p.lanes;
-    while (rows > least && ((p.len + rows - 1) / rows * samples < kBwdParts || rows > p.len)) rows /= 2;
+    while (rows > least && ((p.len + rows - 1) / rows * samples < kJoinParts || rows > p.len)) rows /= 2;
     p.rows = int32_t(rows < least ? least : rows);
     p.block = p.rows * p.lanes;
     p.groups = (p.len + p.rows - 1) / p.rows;
     p.split = join_split(p.groups, samples);
     p.chunks = p.split * samples;
-    p.grid = p.chunks < kBwdParts ? p.chunks : kBwdParts;
+    p.grid = p.chunks < kJoinParts ? p.chunks : kJoinParts;
     return p;
 }
 
 hipError_t launch_join_fwd(const JoinArgs& a, int x_dtype, int r_dtype, const RowPlan& p, hipStream_t st);
 
 // The gradients and partial sums in one kernel.
-hipError_t launch_join_bwd(const JoinBwdArgs& a, int x_dtype, int r_dtype, const JoinPlan& p, hipStream_t st);
+hipError_t launch_join_bwd_16(const JoinBwdArgs& a, int x_dtype, const JoinPlan& p, hipStream_t st);
+hipError_t launch_join_bwd_mixed(const JoinBwdArgs& a, int x_dtype, const JoinPlan& p, hipStream_t st);
+hipError_t launch_join_bwd_f32(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st);
+inline hipError_t launch_join_bwd(const JoinBwdArgs& a, int x_dtype, int r_dtype, const JoinPlan& p, hipStream_t st)
+{
+    return x_dtype == GN_F32   ? launch_join_bwd_f32(a, p, st)
+           : r_dtype == GN_F32 ? launch_join_bwd_mixed(a, x_dtype, p, st)
+                               : launch_join_bwd_16(a, x_dtype, p, st);
+}
 // Of wide rows: their means (a.row), then the gradients and partial sums.
 hipError_t launch_join_bwd_wide(const JoinBwdArgs& a, int x_dtype, int r_dtype, hipStream_t st);
 

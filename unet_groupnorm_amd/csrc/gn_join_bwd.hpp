@@ -1,5 +1,6 @@
-// gn_join_bwd.hip -- backward of the residual join over rows that fit a workgroup's registers, from
-// its saved tensors or their 8-bit checkpoints.
+// gn_join_bwd.hpp -- backward of the residual join over rows that fit a workgroup's registers, from
+// its saved tensors or their 8-bit checkpoints; compiled by gn_join_bwd_16.hip, gn_join_bwd_mixed.hip
+// and gn_join_bwd_f32.hip for their types.
 //
 //   d    = rstd * (dy * m - xhat * c1) + dh,   c1 = mean(dy * m * xhat)
 //   dres = residual_scale * d,   dx = post_rstd * (d * c - xpost * c2),   c2 = mean(d * c * xpost)
@@ -8,6 +9,8 @@
 // c2 needs d and d needs c1, two reductions one after the other; but d is linear in c1, so
 // c2 = mean((rstd * dy * m + dh) * c * xpost) - rstd * c1 * mean(xhat * c * xpost), and one
 // reduction of three sums gives both: one barrier a row.
+#pragma once
+
 #include "gn_join_vec.hpp"
 
 namespace gn {
@@ -38,6 +41,19 @@ __device__ __forceinline__ void row_sums(float (&v)[3], const Row<W>& r, uint32_
     }
 }
 
+// Keeps the compiler from moving what makes v behind what follows, or loads that follow in front of it.
+template <int W>
+__device__ __forceinline__ void pin(float (&v)[W])
+{
+#pragma unroll
+    for (int e = 0; e < W; ++e) asm volatile("" : "+v"(v[e])::"memory");
+}
+
+// How rows end, beside gn_rows.hpp's ways: lanes at and behind a row's end, which read its last W
+// columns, also compute and store them, the bits that their owners store; only the sums leave them
+// out. So no branch leads round the stores.
+constexpr int kWhole = 3;
+
 // A workgroup's walk over the row groups of its chunks.
 struct Walk {
     int64_t chunk, n, g;  // n: the chunk's sequence, g: the group within it
@@ -60,12 +76,20 @@ struct Walk {
 // Workgroup b takes the chunks b, b + gridDim.x, ... (a.rows rows at once, a.lanes lanes each; MANY:
 // more than 64). DEPTH groups' loads are in flight behind the one in use. Every lane keeps its
 // columns' vectors and sums in registers; at a chunk's end the workgroup adds its rows' sums in LDS
-// and leaves two partial sums for each column. FULL: dy, dh, h and x are all there; else each may be
-// missing, behind branches. NT: nontemporal loads.
+// and leaves two partial sums for each column. FULL: dy, dh, h, x, dx and dres are all there; else
+// each may be missing, behind branches. NT: nontemporal loads.
+//
+// A group's values are widened before the next group is loaded into the registers that they came in
+// (pin): otherwise the compiler loads into others and copies them at the loop's end, for which it
+// waits there. And a wait for those loads is not one for the stores behind them as long as no branch
+// leads round the stores: a group's rows behind the sequence's end, which are its last row once
+// more, store that row's bits once more (MANY; the barrier orders them behind the loads).
 template <typename XT, typename HT, bool CK, bool FULL, int W, int V, bool MANY, int END, int DEPTH, bool NT>
 __global__ void __launch_bounds__(kBwdBlock)
 join_bwd_kernel(JoinBwdArgs a)
 {
+    constexpr int E = END == kWhole ? kEnds : END;        // for loads and partial sums
+    constexpr int kWiden = END == kWhole ? kExact : END;  // columns of others are wanted too
     __shared__ uint32_t s_sum[2][3 * (kBwdBlock / 64)];
     __shared__ __align__(16) float s_part[kBwdBlock * W];
     int32_t sub = int32_t(threadIdx.x) / a.lanes;
@@ -78,7 +102,9 @@ join_bwd_kernel(JoinBwdArgs a)
         Saved<XT, W, CK> x[V];
         float rstd, post_rstd;
     };
-    const bool has_dy = FULL || a.dy, has_dh = FULL || a.dh, has_x = FULL || a.x;
+    const bool has_dy = FULL || a.dy, has_dh = FULL || a.dh, has_x = FULL || a.x, has_dx = FULL || a.dx,
+               has_dres = FULL || a.dres;
+    const float* post_rstd_at = a.post ? a.post_rstd : a.rstd;  // one to read in any case
     Walk use, next;
     use.start(a, blockIdx.x);
     next = use;
@@ -92,24 +118,24 @@ join_bwd_kernel(JoinBwdArgs a)
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             const int32_t i = r.piece(u);
-            if (has_dy) load_piece<XT, W, END, NT>(in<XT>(a.dy) + k, r, i, l.dy[u]);
-            if (has_dh) load_piece<HT, W, END, NT>(in<HT>(a.dh) + k, r, i, l.dh[u]);
-            if (has_dy) l.h[u].template load<END, NT>(a.h, k, r, i, a.h_scale, ks, a.block);
-            if (has_x) l.x[u].template load<END, NT>(a.x, kx, r, i, a.x_scale, ks, a.block);
+            if (has_dy) load_piece<XT, W, E, NT>(in<XT>(a.dy) + k, r, i, l.dy[u]);
+            if (has_dh) load_piece<HT, W, E, NT>(in<HT>(a.dh) + k, r, i, l.dh[u]);
+            if (has_dy) l.h[u].template load<E, NT>(a.h, k, r, i, a.h_scale, ks, a.block);
+            if (has_x) l.x[u].template load<E, NT>(a.x, kx, r, i, a.x_scale, ks, a.block);
         }
         l.rstd = has_dy ? a.rstd[t] : 0.0f;
-        l.post_rstd = a.post ? a.post_rstd[t] : 1.0f;
+        l.post_rstd = FULL || a.post ? post_rstd_at[t] : 1.0f;
         next.step(a);
     };
     float c[V][W], m[V][W], A[V][W], C[V][W];
     const auto vectors = [&]() {  // of a sequence
         RawVecs<W> rv[V];
 #pragma unroll
-        for (int u = 0; u < V; ++u) rv[u].template load<END>(a.v, use.n, r, r.piece(u));
+        for (int u = 0; u < V; ++u) rv[u].template load<E>(a.v, use.n, r, r.piece(u));
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            rv[u].template branch<END>(a.v, r, r.piece(u), c[u]);
-            rv[u].template multiplier<END>(a.v, r, r.piece(u), m[u]);
+            rv[u].template branch<kWiden>(a.v, r, r.piece(u), c[u]);
+            rv[u].template multiplier<kWiden>(a.v, r, r.piece(u), m[u]);
         }
     };
     const auto zero = [&]() {
@@ -123,7 +149,7 @@ join_bwd_kernel(JoinBwdArgs a)
         part += use.chunk * a.H;
         if (a.rows == 1) {
 #pragma unroll
-            for (int u = 0; u < V; ++u) store_values<float, W, END>(part, r, r.piece(u), sum[u]);
+            for (int u = 0; u < V; ++u) store_values<float, W, E>(part, r, r.piece(u), sum[u]);
             return;
         }
 #pragma unroll
@@ -135,32 +161,51 @@ join_bwd_kernel(JoinBwdArgs a)
             const int32_t first = u * a.lanes * W, n = a.lanes * W;
             for (int32_t k = threadIdx.x; k < n; k += blockDim.x) {
                 const int32_t i = first / W + k / W, e = k % W;
-                if (END == kTiny ? first + k >= r.H : e < r.skip(i)) continue;
+                if (E == kTiny ? first + k >= r.H : e < r.skip(i)) continue;
                 float s = s_part[k];
                 for (int32_t j = 1; j < a.rows; ++j) s = s + s_part[j * n + k];
                 part[r.column(i) + e] = s;
             }
         }
     };
+    const auto store = [&](auto* p, int32_t i, const float (&o)[W]) {
+        using T = typename std::remove_pointer<decltype(p)>::type;
+        if constexpr (END == kWhole) {
+            Piece<T, W> q;
+            q.narrow(o);
+            q.template store<false>(p + r.column(i));
+        } else {
+            store_values<T, W, END>(p, r, i, o);
+        }
+    };
     int phase = 0;
     const auto group = [&](Loaded& l) {
         float dy[V][W], x[V][W], h[V][W], e[V][W];
-        const float rstd = l.rstd, post_rstd = l.post_rstd;
+        float scalar[2] = {l.rstd, a.post ? l.post_rstd : 1.0f};
+        pin(scalar);
+        const float rstd = scalar[0], post_rstd = scalar[1];
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             const int32_t i = r.piece(u);
 #pragma unroll
             for (int k = 0; k < W; ++k) dy[u][k] = e[u][k] = h[u][k] = x[u][k] = 0.0f;
-            if (has_dy) widen_piece<XT, W, END>(l.dy[u], r, i, dy[u]);
-            if (has_dh) widen_piece<HT, W, END>(l.dh[u], r, i, e[u]);
-            if (has_dy) l.h[u].template widen<END>(r, i, a.q_dtype, h[u]);
-            if (has_x) l.x[u].template widen<END>(r, i, a.q_dtype, x[u]);
+            if (has_dy) widen_piece<XT, W, kWiden>(l.dy[u], r, i, dy[u]);
+            if (has_dh) widen_piece<HT, W, kWiden>(l.dh[u], r, i, e[u]);
+            if (has_dy) l.h[u].template widen<kWiden>(r, i, a.q_dtype, h[u]);
+            if (has_x) l.x[u].template widen<kWiden>(r, i, a.q_dtype, x[u]);
+            pin(dy[u]);
+            pin(e[u]);
+            pin(h[u]);
+            pin(x[u]);
         }
         load(l);
-        const int64_t t = row(use), at = t * a.H;
-        const bool live = t < (use.n + 1) * a.len;
+        const int64_t end = (use.n + 1) * a.len;
+        int64_t t = row(use);
+        const bool live = t < end;
+        t = live ? t : end - 1;
+        const int64_t at = t * a.H;
         float v[3] = {0.0f, 0.0f, 0.0f};
-        if (live) {
+        if (MANY || live) {
 #pragma unroll
             for (int u = 0; u < V; ++u) {
                 float g[W], cx[W];
@@ -168,19 +213,31 @@ join_bwd_kernel(JoinBwdArgs a)
                 for (int k = 0; k < W; ++k) {
                     h[u][k] = h[u][k] * rstd;  // xhat
                     x[u][k] = x[u][k] * post_rstd;  // xpost
-                    A[u][k] = fmaf(dy[u][k], h[u][k], A[u][k]);
+                    if (live) A[u][k] = fmaf(dy[u][k], h[u][k], A[u][k]);
                     g[k] = dy[u][k] * m[u][k];
                     e[u][k] = fmaf(rstd, g[k], e[u][k]);
                     cx[k] = c[u][k] * x[u][k];
                 }
-                v[0] = v[0] + tree_sumprod(g, h[u]);
+                float xh[W];
+#pragma unroll
+                for (int k = 0; k < W; ++k) xh[k] = h[u][k];
+                if (END == kWhole && r.piece(u) >= r.full) {
+                    const int32_t skip = r.skip(r.piece(u));
+#pragma unroll
+                    for (int k = 0; k < W; ++k) {
+                        xh[k] = k < skip ? 0.0f : xh[k];
+                        cx[k] = k < skip ? 0.0f : cx[k];
+                        g[k] = k < skip ? 0.0f : g[k];
+                    }
+                }
+                v[0] = v[0] + tree_sumprod(g, xh);
                 v[1] = v[1] + tree_sumprod(e[u], cx);
-                v[2] = v[2] + tree_sumprod(h[u], cx);
+                v[2] = v[2] + tree_sumprod(xh, cx);
             }
         }
         row_sums<MANY>(v, r, s_sum[phase] + (MANY ? 3 * sub * (r.lanes >> 6) : 0));
         phase ^= 1;
-        if (live) {  // behind the row's barrier
+        if (MANY || live) {  // behind the row's barrier
             const float c1 = v[0] * a.inv_H * rstd, c2 = fmaf(-c1, v[2], v[1]) * a.inv_H;
 #pragma unroll
             for (int u = 0; u < V; ++u) {
@@ -191,10 +248,10 @@ join_bwd_kernel(JoinBwdArgs a)
                 }
 #pragma unroll
                 for (int k = 0; k < W; ++k) {
-                    C[u][k] = fmaf(e[u][k], x[u][k], C[u][k]);
+                    if (live) C[u][k] = fmaf(e[u][k], x[u][k], C[u][k]);
                     o[k] = a.residual_scale * e[u][k];
                 }
-                if (a.dres) store_values<HT, W, END>(out<HT>(a.dres) + at, r, r.piece(u), o);
+                if (has_dres) store(out<HT>(a.dres) + at, r.piece(u), o);
                 if (a.post) {
 #pragma unroll
                     for (int k = 0; k < W; ++k) o[k] = post_rstd * fmaf(-x[u][k], c2, e[u][k] * c[u][k]);
@@ -202,7 +259,7 @@ join_bwd_kernel(JoinBwdArgs a)
 #pragma unroll
                     for (int k = 0; k < W; ++k) o[k] = e[u][k] * c[u][k];
                 }
-                if (a.dx) store_values<XT, W, END>(out<XT>(a.dx) + at, r, r.piece(u), o);
+                if (has_dx) store(out<XT>(a.dx) + at, r.piece(u), o);
             }
         }
         const Walk was = use;
@@ -236,12 +293,15 @@ template <typename XT, typename HT, int W, bool CK>
 hipError_t one(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st)
 {
     const dim3 grid = dim3(unsigned(p.grid)), block = dim3(p.block);
-    const bool full = a.dy && a.dh && a.x;
+    const bool full = a.dy && a.dh && a.x && a.dx && a.dres;
     const auto go = [&](auto v, auto end) {
         constexpr int V = decltype(v)::value, E = decltype(end)::value, kDepth = V * W <= 8 ? 2 : 1;
         const auto with = [&](auto many) {
             constexpr bool M = decltype(many)::value;
             if (!full) return launch(join_bwd_kernel<XT, HT, CK, false, W, V, M, E == kTiny ? kTiny : kEnds, 1, false>, grid, block, st, a);
+            // a shorter last piece may lie in two blocks of a checkpoint, whose scales its lane has not both
+            if constexpr (CK && E == kWhole)
+                if (a.H % W && a.block) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, kEnds, kDepth, false>, grid, block, st, a);
             if constexpr (E == kExact)
                 if (a.nt) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, true>, grid, block, st, a);
             return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, false>, grid, block, st, a);
@@ -254,7 +314,7 @@ hipError_t one(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st)
             return with(std::true_type{});
     };
     using Exact = std::integral_constant<int, kExact>;
-    using Ends = std::integral_constant<int, kEnds>;
+    using Ends = std::integral_constant<int, kWhole>;
     if (a.H < W) return go(std::integral_constant<int, 1>{}, std::integral_constant<int, kTiny>{});
     const auto pieces = [&](auto v) { return p.exact ? go(v, Exact{}) : go(v, Ends{}); };
     if (p.vecs == 1) return pieces(std::integral_constant<int, 1>{});
@@ -271,12 +331,5 @@ hipError_t one(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st)
 }
 
 }  // namespace
-
-hipError_t launch_join_bwd(const JoinBwdArgs& a, int x_dtype, int r_dtype, const JoinPlan& p, hipStream_t st)
-{
-    if (x_dtype == GN_F32) return one<float, float, 4>(a, p, st);
-    if (r_dtype == GN_F32) return x_dtype == GN_BF16 ? one<uint16_t, float, 4>(a, p, st) : one<_Float16, float, 4>(a, p, st);
-    return x_dtype == GN_BF16 ? one<uint16_t, uint16_t, 8>(a, p, st) : one<_Float16, _Float16, 8>(a, p, st);
-}
 
 }  // namespace gn

@@ -1,6 +1,6 @@
 // gn_join_wide.hip -- backward of the residual join over rows too wide for a workgroup's registers, in
 // two kernels: the rows' means, then the gradients and the sums over rows, columns by columns
-// (gn_join_bwd.hip has the formulas); and the vectors' gradients from the partial sums of both.
+// (gn_join_bwd.hpp has the formulas); and the vectors' gradients from the partial sums of both.
 #include "gn_join_vec.hpp"
 
 namespace gn {
