@@ -105,14 +105,22 @@ inline int64_t join_split(int64_t groups, int64_t samples)
     return split;
 }
 
+// Threads of the backward's workgroup, by the columns of a lane.
+constexpr int32_t join_block(int32_t columns) { return columns <= 8 ? 768 : kBwdBlock; }
+
 inline JoinPlan join_plan(int64_t T, int64_t H, int64_t samples, bool fp32)
 {
     JoinPlan p;
     static_cast<RowPlan&>(p) = row_plan(H, fp32, true);
+    if (p.width == 8 && p.vecs == 2 && H <= 4096) {
+        p.vecs = 1;
+        p.lanes = int32_t(((H + 7) / 8 + 63) / 64 * 64);
+        p.exact = int64_t(p.lanes) * 8 == H;
+    }
     p.wide = p.vecs * p.width > 16 || p.lanes > kBwdBlock;
     p.len = samples > 0 ? T / samples : 0;
     const int32_t least = p.lanes < 64 ? 64 / p.lanes : 1;  // rows of a whole wave
-    int64_t rows = p.wide ? 1 : kBwdBlock / p.lanes;
+    int64_t rows = p.wide ? 1 : join_block(p.vecs * p.width) / p.lanes;
     while (rows > least && ((p.len + rows - 1) / rows * samples < kJoinParts || rows > p.len)) rows /= 2;
     p.rows = int32_t(rows < least ? least : rows);
     p.block = p.rows * p.lanes;

@@ -27,7 +27,7 @@ __device__ __forceinline__ void row_sums(float (&v)[3], const Row<W>& r, uint32_
         for (int q = 0; q < 3; ++q) v[q] = __uint_as_float(lanes_all<AddOp>(__float_as_uint(v[q]), r.lanes));
         return;
     }
-    const int nw = r.lanes >> 6, k = r.lane & 7;  // 8 waves at most
+    const int nw = r.lanes >> 6, k = r.lane & 7;  // 512 lanes at most
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
         const uint32_t b = lanes_all<AddOp>(__float_as_uint(v[q]), 64);
@@ -47,6 +47,15 @@ __device__ __forceinline__ void pin(float (&v)[W])
 {
 #pragma unroll
     for (int e = 0; e < W; ++e) asm volatile("" : "+v"(v[e])::"memory");
+}
+
+// The lane's view of the row again, for the compiler another one: what it derives from this is computed
+// where it is needed, not kept in registers over the loop.
+template <int W>
+__device__ __forceinline__ Row<W> again(Row<W> r)
+{
+    asm volatile("" : "+v"(r.lane));
+    return r;
 }
 
 // How rows end, beside gn_rows.hpp's ways: lanes at and behind a row's end, which read its last W
@@ -74,7 +83,7 @@ struct Walk {
 };
 
 // Workgroup b takes the chunks b, b + gridDim.x, ... (a.rows rows at once, a.lanes lanes each; MANY:
-// more than 64). DEPTH groups' loads are in flight behind the one in use. Every lane keeps its
+// more than 64). The next group's loads are in flight behind the one in use. Every lane keeps its
 // columns' vectors and sums in registers; at a chunk's end the workgroup adds its rows' sums in LDS
 // and leaves two partial sums for each column. FULL: dy, dh, h, x, dx and dres are all there; else
 // each may be missing, behind branches. NT: nontemporal loads.
@@ -84,14 +93,15 @@ struct Walk {
 // waits there. And a wait for those loads is not one for the stores behind them as long as no branch
 // leads round the stores: a group's rows behind the sequence's end, which are its last row once
 // more, store that row's bits once more (MANY; the barrier orders them behind the loads).
-template <typename XT, typename HT, bool CK, bool FULL, int W, int V, bool MANY, int END, int DEPTH, bool NT>
-__global__ void __launch_bounds__(kBwdBlock)
+template <typename XT, typename HT, bool CK, bool FULL, int W, int V, bool MANY, int END, bool NT>
+__global__ void __launch_bounds__(join_block(V * W))
 join_bwd_kernel(JoinBwdArgs a)
 {
     constexpr int E = END == kWhole ? kEnds : END;        // for loads and partial sums
     constexpr int kWiden = END == kWhole ? kExact : END;  // columns of others are wanted too
-    __shared__ uint32_t s_sum[2][3 * (kBwdBlock / 64)];
-    __shared__ __align__(16) float s_part[kBwdBlock * W];
+    constexpr int kBlock = join_block(V * W);
+    __shared__ uint32_t s_sum[2][3 * (kBlock / 64)];
+    __shared__ __align__(16) float s_part[kBlock * W];
     int32_t sub = int32_t(threadIdx.x) / a.lanes;
     if (MANY) sub = __builtin_amdgcn_readfirstlane(sub);
     const Row<W> r = row_of<W>(a.H, a.lanes, int32_t(threadIdx.x) - sub * a.lanes);
@@ -115,27 +125,50 @@ join_bwd_kernel(JoinBwdArgs a)
         int64_t t = row(next);
         t = t < end ? t : end - 1;
         const int64_t k = t * a.H, kx = t * a.x_stride, ks = t * a.scales;
+        const Row<W> q = again(r);
+        l.rstd = has_dy ? a.rstd[t] : 0.0f;  // first, as they are waited for first
+        l.post_rstd = FULL || a.post ? post_rstd_at[t] : 1.0f;
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const int32_t i = r.piece(u);
-            if (has_dy) load_piece<XT, W, E, NT>(in<XT>(a.dy) + k, r, i, l.dy[u]);
-            if (has_dh) load_piece<HT, W, E, NT>(in<HT>(a.dh) + k, r, i, l.dh[u]);
-            if (has_dy) l.h[u].template load<E, NT>(a.h, k, r, i, a.h_scale, ks, a.block);
-            if (has_x) l.x[u].template load<E, NT>(a.x, kx, r, i, a.x_scale, ks, a.block);
+            const int32_t i = q.piece(u);
+            if (has_dy) load_at<XT, W, E, NT>(in<XT>(a.dy) + k, q, i, l.dy[u]);
+            if (has_dh) load_at<HT, W, E, NT>(in<HT>(a.dh) + k, q, i, l.dh[u]);
+            if (has_dy) l.h[u].template load<E, NT>(a.h, k, q, i, a.h_scale, ks, a.block);
+            if (has_x) l.x[u].template load<E, NT>(a.x, kx, q, i, a.x_scale, ks, a.block);
         }
-        l.rstd = has_dy ? a.rstd[t] : 0.0f;
-        l.post_rstd = FULL || a.post ? post_rstd_at[t] : 1.0f;
         next.step(a);
     };
     float c[V][W], m[V][W], A[V][W], C[V][W];
-    const auto vectors = [&]() {  // of a sequence
-        RawVecs<W> rv[V];
-#pragma unroll
-        for (int u = 0; u < V; ++u) rv[u].template load<E>(a.v, use.n, r, r.piece(u));
+    // The vectors of a sequence, two by two.
+    RawVec<W> rv[2][V];
+    const auto load_branch = [&]() {
+        const Row<W> q = again(r);
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            rv[u].template branch<kWiden>(a.v, r, r.piece(u), c[u]);
-            rv[u].template multiplier<kWiden>(a.v, r, r.piece(u), m[u]);
+            rv[0][u].template load<E>(vector_of(a.v.gate, use.n), a.v.gate.dtype, q, q.piece(u));
+            rv[1][u].template load<E>(a.v.post.p, a.v.post.dtype, q, q.piece(u));
+        }
+    };
+    const auto load_multiplier = [&](RawVec<W> (&raw)[2][V]) {
+        const Row<W> q = again(r);
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            raw[0][u].template load<E>(a.v.w.p, a.v.w.dtype, q, q.piece(u));
+            raw[1][u].template load<E>(vector_of(a.v.scale, use.n), a.v.scale.dtype, q, q.piece(u));
+        }
+    };
+    const auto take_branch = [&]() {  // waited for here (pin), not in the loop
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            branch_of<kWiden>(a.v, rv[0][u], rv[1][u], r, r.piece(u), c[u]);
+            pin(c[u]);
+        }
+    };
+    const auto take_multiplier = [&](const RawVec<W> (&raw)[2][V]) {
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            multiplier_of<kWiden>(a.v, raw[0][u], raw[1][u], r, r.piece(u), m[u]);
+            pin(m[u]);
         }
     };
     const auto zero = [&]() {
@@ -147,9 +180,10 @@ join_bwd_kernel(JoinBwdArgs a)
     // A chunk's partial sums of one kind, to part[chunk]. s_part is free after another barrier.
     const auto leave = [&](float* part, const float (&sum)[V][W]) {
         part += use.chunk * a.H;
+        const Row<W> q = again(r);
         if (a.rows == 1) {
 #pragma unroll
-            for (int u = 0; u < V; ++u) store_values<float, W, E>(part, r, r.piece(u), sum[u]);
+            for (int u = 0; u < V; ++u) store_values<float, W, E>(part, q, q.piece(u), sum[u]);
             return;
         }
 #pragma unroll
@@ -161,21 +195,21 @@ join_bwd_kernel(JoinBwdArgs a)
             const int32_t first = u * a.lanes * W, n = a.lanes * W;
             for (int32_t k = threadIdx.x; k < n; k += blockDim.x) {
                 const int32_t i = first / W + k / W, e = k % W;
-                if (E == kTiny ? first + k >= r.H : e < r.skip(i)) continue;
+                if (E == kTiny ? first + k >= q.H : e < q.skip(i)) continue;
                 float s = s_part[k];
                 for (int32_t j = 1; j < a.rows; ++j) s = s + s_part[j * n + k];
-                part[r.column(i) + e] = s;
+                part[q.column(i) + e] = s;
             }
         }
     };
-    const auto store = [&](auto* p, int32_t i, const float (&o)[W]) {
+    const auto store = [&](auto* p, const Row<W>& q, int32_t i, const float (&o)[W]) {
         using T = typename std::remove_pointer<decltype(p)>::type;
-        if constexpr (END == kWhole) {
-            Piece<T, W> q;
-            q.narrow(o);
-            q.template store<false>(p + r.column(i));
+        if constexpr (END == kWhole || END == kExact) {
+            Piece<T, W> w;
+            w.narrow(o);
+            w.template store<false>(element(p, first_column<W, E>(q, i)));
         } else {
-            store_values<T, W, END>(p, r, i, o);
+            store_values<T, W, END>(p, q, i, o);
         }
     };
     int phase = 0;
@@ -218,26 +252,23 @@ join_bwd_kernel(JoinBwdArgs a)
                     e[u][k] = fmaf(rstd, g[k], e[u][k]);
                     cx[k] = c[u][k] * x[u][k];
                 }
-                float xh[W];
-#pragma unroll
-                for (int k = 0; k < W; ++k) xh[k] = h[u][k];
                 if (END == kWhole && r.piece(u) >= r.full) {
                     const int32_t skip = r.skip(r.piece(u));
 #pragma unroll
                     for (int k = 0; k < W; ++k) {
-                        xh[k] = k < skip ? 0.0f : xh[k];
-                        cx[k] = k < skip ? 0.0f : cx[k];
                         g[k] = k < skip ? 0.0f : g[k];
+                        cx[k] = k < skip ? 0.0f : cx[k];
                     }
                 }
-                v[0] = v[0] + tree_sumprod(g, xh);
+                v[0] = v[0] + tree_sumprod(g, h[u]);
                 v[1] = v[1] + tree_sumprod(e[u], cx);
-                v[2] = v[2] + tree_sumprod(xh, cx);
+                v[2] = v[2] + tree_sumprod(h[u], cx);
             }
         }
         row_sums<MANY>(v, r, s_sum[phase] + (MANY ? 3 * sub * (r.lanes >> 6) : 0));
         phase ^= 1;
         if (MANY || live) {  // behind the row's barrier
+            const Row<W> q = again(r);
             const float c1 = v[0] * a.inv_H * rstd, c2 = fmaf(-c1, v[2], v[1]) * a.inv_H;
 #pragma unroll
             for (int u = 0; u < V; ++u) {
@@ -251,7 +282,7 @@ join_bwd_kernel(JoinBwdArgs a)
                     if (live) C[u][k] = fmaf(e[u][k], x[u][k], C[u][k]);
                     o[k] = a.residual_scale * e[u][k];
                 }
-                if (has_dres) store(out<HT>(a.dres) + at, r.piece(u), o);
+                if (has_dres) store(out<HT>(a.dres) + at, q, q.piece(u), o);
                 if (a.post) {
 #pragma unroll
                     for (int k = 0; k < W; ++k) o[k] = post_rstd * fmaf(-x[u][k], c2, e[u][k] * c[u][k]);
@@ -259,7 +290,7 @@ join_bwd_kernel(JoinBwdArgs a)
 #pragma unroll
                     for (int k = 0; k < W; ++k) o[k] = e[u][k] * c[u][k];
                 }
-                if (has_dx) store(out<XT>(a.dx) + at, r.piece(u), o);
+                if (has_dx) store(out<XT>(a.dx) + at, q, q.piece(u), o);
             }
         }
         const Walk was = use;
@@ -272,21 +303,31 @@ join_bwd_kernel(JoinBwdArgs a)
                 use = now;
             }
             zero();
-            if (use.chunk < a.chunks && use.n != was.n) vectors();
+            if (use.chunk < a.chunks && use.n != was.n) {
+                load_branch();
+                take_branch();
+                load_multiplier(rv);
+                take_multiplier(rv);
+            }
         }
     };
-    vectors();  // first: behind rows in flight they would wait for those
-    zero();
-    Loaded l[DEPTH];
-#pragma unroll
-    for (int k = 0; k < DEPTH; ++k) load(l[k]);
-    while (use.chunk < a.chunks) {
-#pragma unroll
-        for (int k = 0; k < DEPTH; ++k) {
-            if (k && use.chunk >= a.chunks) break;
-            group(l[k]);
-        }
+    // The vectors first: behind the rows they would wait for those.
+    Loaded l;
+    load_branch();
+    if constexpr (V * W <= 8) {
+        RawVec<W> more[2][V];
+        load_multiplier(more);
+        load(l);
+        take_branch();
+        take_multiplier(more);
+    } else {  // no registers for all at once
+        take_branch();
+        load_multiplier(rv);
+        load(l);
+        take_multiplier(rv);
     }
+    zero();
+    while (use.chunk < a.chunks) group(l);
 }
 
 template <typename XT, typename HT, int W, bool CK>
@@ -295,16 +336,16 @@ hipError_t one(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st)
     const dim3 grid = dim3(unsigned(p.grid)), block = dim3(p.block);
     const bool full = a.dy && a.dh && a.x && a.dx && a.dres;
     const auto go = [&](auto v, auto end) {
-        constexpr int V = decltype(v)::value, E = decltype(end)::value, kDepth = V * W <= 8 ? 2 : 1;
+        constexpr int V = decltype(v)::value, E = decltype(end)::value;
         const auto with = [&](auto many) {
             constexpr bool M = decltype(many)::value;
-            if (!full) return launch(join_bwd_kernel<XT, HT, CK, false, W, V, M, E == kTiny ? kTiny : kEnds, 1, false>, grid, block, st, a);
+            if (!full) return launch(join_bwd_kernel<XT, HT, CK, false, W, V, M, E == kTiny ? kTiny : kEnds, false>, grid, block, st, a);
             // a shorter last piece may lie in two blocks of a checkpoint, whose scales its lane has not both
             if constexpr (CK && E == kWhole)
-                if (a.H % W && a.block) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, kEnds, kDepth, false>, grid, block, st, a);
+                if (a.H % W && a.block) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, kEnds, false>, grid, block, st, a);
             if constexpr (E == kExact)
-                if (a.nt) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, true>, grid, block, st, a);
-            return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, false>, grid, block, st, a);
+                if (a.nt) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, true>, grid, block, st, a);
+            return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, false>, grid, block, st, a);
         };
         if constexpr (V == 1)
             if (p.lanes <= 64) return with(std::false_type{});

@@ -9,6 +9,31 @@ namespace gn {
 
 namespace {
 
+// Element c of the row at p by its distance in bytes, 32 bits of it: where p is the same for all lanes,
+// an access is then a scalar address and one register, not two registers for each access.
+template <typename T>
+__device__ __forceinline__ T* element(T* p, int32_t c)
+{
+    using Byte = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+    return reinterpret_cast<T*>(reinterpret_cast<Byte*>(p) + uint32_t(c) * uint32_t(sizeof(T)));
+}
+
+// The first column that a lane reads for piece i.
+template <int W, int END>
+__device__ __forceinline__ int32_t first_column(const Row<W>& r, int32_t i)
+{
+    return END == kExact ? i * W : r.column(i);
+}
+
+template <typename T, int W, int END, bool NT>
+__device__ __forceinline__ void load_at(const T* p, const Row<W>& r, int32_t i, Piece<T, W>& raw)
+{
+    if (END == kTiny)
+        raw.load_part(p, i == 0 ? r.H : 0);
+    else
+        raw.template load<NT>(element(p, first_column<W, END>(r, i)));
+}
+
 // v's vector of sequence n.
 __device__ __forceinline__ const void* vector_of(const JoinVec& v, int64_t n)
 {
@@ -32,18 +57,18 @@ struct RawVec {
             for (int e = 0; e < W; ++e) w[e] = __float_as_uint(v[e]);
             return;
         }
-        const int32_t c = END == kExact ? i * W : r.column(i);
+        const int32_t c = first_column<W, END>(r, i);
         if (dtype == GN_F32) {
 #pragma unroll
             for (int k = 0; k < W; k += 4) {
                 Piece<float, 4> q;
-                q.load<false>(in<float>(p) + c + k);
+                q.load<false>(element(in<float>(p), c + k));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[k + e] = q.w[e];
             }
         } else {
             Piece<uint16_t, W> q;
-            q.template load<false>(in<uint16_t>(p) + c);
+            q.template load<false>(element(in<uint16_t>(p), c));
 #pragma unroll
             for (int e = 0; e < W / 2; ++e) w[e] = q.w[e];
         }
@@ -78,6 +103,30 @@ struct RawVec {
     }
 };
 
+// Piece i of the coefficient c = (branch_scale * gate) * post_weight.
+template <int END, int W>
+__device__ __forceinline__ void branch_of(const JoinVecs& j, const RawVec<W>& gate, const RawVec<W>& post, const Row<W>& r,
+                                          int32_t i, float (&c)[W])
+{
+    float p[W];
+    gate.template widen<END>(j.gate.p, j.gate.dtype, r, i, 1.0f, c);
+    post.template widen<END>(j.post.p, j.post.dtype, r, i, 1.0f, p);
+#pragma unroll
+    for (int e = 0; e < W; ++e) c[e] = j.branch_scale * c[e] * p[e];
+}
+
+// Piece i of the multiplier m = weight * (1 + scale).
+template <int END, int W>
+__device__ __forceinline__ void multiplier_of(const JoinVecs& j, const RawVec<W>& w, const RawVec<W>& scale, const Row<W>& r,
+                                              int32_t i, float (&m)[W])
+{
+    float s[W];
+    w.template widen<END>(j.w.p, j.w.dtype, r, i, 1.0f, m);
+    scale.template widen<END>(j.scale.p, j.scale.dtype, r, i, 0.0f, s);
+#pragma unroll
+    for (int e = 0; e < W; ++e) m[e] = m[e] * (1.0f + s[e]);
+}
+
 // A piece of the four vectors of sequence n.
 template <int W>
 struct RawVecs {
@@ -90,25 +139,15 @@ struct RawVecs {
         w.template load<END>(j.w.p, j.w.dtype, r, i);
         scale.template load<END>(vector_of(j.scale, n), j.scale.dtype, r, i);
     }
-    // The coefficient c = (branch_scale * gate) * post_weight.
     template <int END>
     __device__ __forceinline__ void branch(const JoinVecs& j, const Row<W>& r, int32_t i, float (&c)[W]) const
     {
-        float p[W];
-        gate.template widen<END>(j.gate.p, j.gate.dtype, r, i, 1.0f, c);
-        post.template widen<END>(j.post.p, j.post.dtype, r, i, 1.0f, p);
-#pragma unroll
-        for (int e = 0; e < W; ++e) c[e] = j.branch_scale * c[e] * p[e];
+        branch_of<END>(j, gate, post, r, i, c);
     }
-    // The multiplier m = weight * (1 + scale).
     template <int END>
     __device__ __forceinline__ void multiplier(const JoinVecs& j, const Row<W>& r, int32_t i, float (&m)[W]) const
     {
-        float s[W];
-        w.template widen<END>(j.w.p, j.w.dtype, r, i, 1.0f, m);
-        scale.template widen<END>(j.scale.p, j.scale.dtype, r, i, 0.0f, s);
-#pragma unroll
-        for (int e = 0; e < W; ++e) m[e] = m[e] * (1.0f + s[e]);
+        multiplier_of<END>(j, w, scale, r, i, m);
     }
 };
 
@@ -126,7 +165,7 @@ struct Saved {
     __device__ __forceinline__ void load(const void* p, int64_t at, const Row<W>& r, int32_t i, const float*, int64_t,
                                          int32_t)
     {
-        load_piece<T, W, END, NT>(in<T>(p) + at, r, i, raw);
+        load_at<T, W, END, NT>(in<T>(p) + at, r, i, raw);
     }
     template <int END>
     __device__ __forceinline__ void widen(const Row<W>& r, int32_t i, int, float (&v)[W]) const
@@ -159,10 +198,10 @@ struct Saved<T, W, true> {
             s = scale[s_at];  // fewer columns than a piece: one scale
             return;
         }
-        const WordsAny* w = reinterpret_cast<const WordsAny*>(q + (END == kExact ? i * W : r.column(i)));
+        const WordsAny* w = reinterpret_cast<const WordsAny*>(element(q, first_column<W, END>(r, i)));
         b = NT ? __builtin_nontemporal_load(w) : *w;
         const int32_t last = END == kExact || r.tail ? r.full : r.full - 1;  // the row's last piece
-        s = scale[s_at + (block ? (END == kExact || i <= last ? i : last) * W / block : 0)];
+        s = *element(scale + s_at, block ? int32_t(uint32_t((END == kExact || i <= last ? i : last) * W) / uint32_t(block)) : 0);
     }
     template <int END>
     __device__ __forceinline__ void widen(const Row<W>& r, int32_t i, int q_dtype, float (&v)[W]) const

@@ -43,8 +43,8 @@ struct JoinPiece {
         Piece<HT, W> rdh;
         Saved<HT, W, CK> rh;
         Saved<XT, W, CK> rx;
-        if (a.dy) load_piece<XT, W, END, false>(in<XT>(a.dy) + t * a.H, r, i, rdy);
-        if (a.dh) load_piece<HT, W, END, false>(in<HT>(a.dh) + t * a.H, r, i, rdh);
+        if (a.dy) load_at<XT, W, END, false>(in<XT>(a.dy) + t * a.H, r, i, rdy);
+        if (a.dh) load_at<HT, W, END, false>(in<HT>(a.dh) + t * a.H, r, i, rdh);
         if (a.dy) rh.template load<END, false>(a.h, t * a.H, r, i, a.h_scale, t * a.scales, a.block);
         if (a.x) rx.template load<END, false>(a.x, t * a.x_stride, r, i, a.x_scale, t * a.scales, a.block);
         RawVecs<W> rv;
