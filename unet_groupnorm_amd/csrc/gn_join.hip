@@ -16,143 +16,225 @@ namespace {
 
 constexpr int kRowMaxWaves = kRowMaxBlock / 64;
 
-// A row's sum and its largest magnitude (bits), over all its lanes with one barrier.
-template <int W>
-__device__ __forceinline__ void row_sum_max(float& sum, uint32_t& top, bool many, const Row<W>& r, uint32_t* s)
+// R rows' sums and, with TOP, their largest magnitudes (bits), over all their lanes with one barrier.
+template <int R, bool MANY, bool TOP, int W>
+__device__ __forceinline__ void rows_all(float (&sum)[R], uint32_t (&top)[R], const Row<W>& r, uint32_t (*s)[2 * kRowMaxWaves])
 {
-    uint32_t a = __float_as_uint(sum);
-    if (!many) {
-        sum = __uint_as_float(lanes_all<AddOp>(a, r.lanes));
-        top = lanes_all<MaxBitsOp>(top, r.lanes);
-        return;
+    const int32_t lanes = MANY ? 64 : r.lanes;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        sum[j] = __uint_as_float(lanes_all<AddOp>(__float_as_uint(sum[j]), lanes));
+        if (TOP) top[j] = lanes_all<MaxBitsOp>(top[j], lanes);
     }
-    a = lanes_all<AddOp>(a, 64);
-    top = lanes_all<MaxBitsOp>(top, 64);
-    if ((r.lane & 63) == 0) {
-        s[r.lane >> 6] = a;
-        s[kRowMaxWaves + (r.lane >> 6)] = top;
-    }
+    if (!MANY) return;
+    if ((r.lane & 63) == 0)
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            s[j][r.lane >> 6] = __float_as_uint(sum[j]);
+            if (TOP) s[j][kRowMaxWaves + (r.lane >> 6)] = top[j];
+        }
     __syncthreads();
-    const int nw = r.lanes >> 6, k = r.lane & 15;
-    a = s[k < nw ? k : 0];
-    top = s[kRowMaxWaves + (k < nw ? k : 0)];
-    sum = __uint_as_float(lanes_all<AddOp>(k < nw ? a : 0u, 16));
-    top = lanes_all<MaxBitsOp>(k < nw ? top : 0u, 16);
+    const int nw = r.lanes >> 6, k = r.lane & 15, w = k < nw ? k : 0;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        const uint32_t a = s[j][w];
+        sum[j] = __uint_as_float(lanes_all<AddOp>(k < nw ? a : 0u, 16));
+        if (TOP) {
+            const uint32_t b = s[j][kRowMaxWaves + w];
+            top[j] = lanes_all<MaxBitsOp>(k < nw ? b : 0u, 16);
+        }
+    }
 }
 
-// A lane's pieces v of a row to 8 bits at q, with its scales at scale; top: the bits of the row's
-// largest magnitude, for block == 0.
-template <int W, int V, int END>
+// Bits of the largest magnitude of piece i, from its raw elements and from its values in fp32 (zeros
+// in columns that are not its own).
+template <typename T, int W, int END>
+__device__ __forceinline__ uint32_t own_amax(const Piece<T, W>& raw, const Row<W>& r, int32_t i, const float (&v)[W])
+{
+    if constexpr (sizeof(T) == 2) {
+        if (END == kExact || i < r.full) return piece_amax16(raw);
+    }
+    return piece_amax(v);
+}
+
+// Piece i of the values v to 8 bits; top: the bits of the piece's largest magnitude, or for block == 0
+// the row's.
+template <int W, int END>
 __device__ __forceinline__ void store_checkpoint(uint8_t* q, float* scale, int32_t block, int q_dtype, const Row<W>& r,
-                                                 uint32_t top, const float (&v)[V][W])
+                                                 int32_t i, uint32_t top, const float (&v)[W])
 {
     const int32_t share = lanes_of_scale(block, r);
+    float t[W];
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-        float t[W];
-#pragma unroll
-        for (int e = 0; e < W; ++e) t[e] = v[u][e];
-        const uint32_t m = block ? lanes_all<MaxBitsOp>(piece_amax(t), share) : top;
-        store_q8<W, END>(q, scale, block, r, r.piece(u), share, scale_of(m, q_dtype), q_dtype, t);
-    }
-}
-
-template <int W, int V>
-__device__ __forceinline__ uint32_t lane_amax(const float (&v)[V][W])
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int u = 0; u < V; ++u) m = MaxBitsOp::f(m, piece_amax(v[u]));
-    return m;
+    for (int e = 0; e < W; ++e) t[e] = v[e];
+    const uint32_t m = block ? lanes_all<MaxBitsOp>(top, share) : top;
+    store_q8<W, END>(q, scale, block, r, i, share, scale_of(m, q_dtype), q_dtype, t);
 }
 
 // ------------------------------------------------------------------ join
 
-// h and y are written after the second reduction's barrier: they may take an input's place, and
-// lanes at the row's end read columns of others. CK: checkpoints may be asked for.
-template <typename XT, typename HT, int W, int V, int END, bool CK>
+// A workgroup takes R rows of one sequence in each of its a.rows places. h and y are written after
+// the second reduction's barrier: they may take an input's place, and lanes at the row's end read
+// columns of others. CK: checkpoints may be asked for. MANY: rows of more than 64 lanes, one place.
+template <typename XT, typename HT, int W, int V, int R, bool MANY, int END, bool CK>
 __global__ void __launch_bounds__(kRowMaxBlock)
 join_fwd_kernel(JoinArgs a)
 {
-    __shared__ uint32_t s_x[2 * kRowMaxWaves], s_h[2 * kRowMaxWaves];
-    const int32_t sub = a.lanes > 64 ? 0 : int32_t(threadIdx.x) / a.lanes;
+    __shared__ uint32_t s_x[MANY ? R : 1][2 * kRowMaxWaves], s_h[MANY ? R : 1][2 * kRowMaxWaves];
+    const int32_t sub = MANY ? 0 : int32_t(threadIdx.x) / a.lanes;
     const Row<W> r = row_of<W>(a.H, a.lanes, int32_t(threadIdx.x) - sub * a.lanes);
-    const int64_t t = int64_t(blockIdx.x) * a.rows + sub;
-    if (t >= a.T) return;  // whole rows leave, and with more than 64 lanes whole workgroups
-    const bool many = V > 1 || a.lanes > 64;
-    float x[V][W], h[V][W];
-    Piece<XT, W> rx[V];
-    Piece<HT, W> rr[V];
-    load_row<XT, W, V, END>(in<XT>(a.x) + t * a.x_stride, r, a.nt, rx);
-    load_row<HT, W, V, END>(in<HT>(a.res) + t * a.H, r, a.nt, rr);
-    const int64_t n = a.one ? 0 : sequence_of(a.first + t, a.len);
+    const int64_t group = a.first + blockIdx.x;
+    int64_t n, first, end;
+    if (a.groups) {
+        n = sequence_of(group, a.groups);
+        first = n * a.len + (group - n * a.groups) * (a.rows * R) + sub;
+        end = (n + 1) * a.len;
+    } else {  // sequences shorter than the places of a workgroup; R is 1
+        first = group * a.rows + sub;
+        if (first >= a.T) return;
+        n = sequence_of(first, a.len);
+        end = first + 1;
+    }
+    const auto row = [&](int j) {  // behind the sequence's last row that row again, not stored
+        const int64_t t = first + j * a.rows;
+        return t < end ? t : end - 1;
+    };
+    Piece<XT, W> rx[R][V];
+    Piece<HT, W> rr[R][V];
     RawVecs<W> rv[V];
+    if (a.nt) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            load_row_as<XT, W, V, END, true>(in<XT>(a.x) + row(j) * a.x_stride, r, rx[j]);
+            load_row_as<HT, W, V, END, true>(in<HT>(a.res) + row(j) * a.H, r, rr[j]);
+        }
+        asm volatile("" ::: "memory");
+    } else {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            load_row_as<XT, W, V, END, false>(in<XT>(a.x) + row(j) * a.x_stride, r, rx[j]);
+            load_row_as<HT, W, V, END, false>(in<HT>(a.res) + row(j) * a.H, r, rr[j]);
+        }
+    }
 #pragma unroll
     for (int u = 0; u < V; ++u) rv[u].template load<END>(a.v, n, r, r.piece(u));
-    float ss = 0.0f;
-    uint32_t top = 0;
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-        widen_piece<XT, W, END>(rx[u], r, r.piece(u), x[u]);
-        ss = ss + tree_sumsq(x[u]);
-    }
     const bool row_scale = CK && a.block == 0;
-    float post_rstd = 1.0f;
+    float ss[R], post_rstd[R];
+    uint32_t x_top[R], h_top[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        post_rstd[j] = 1.0f;
+        ss[j] = 0.0f;
+        x_top[j] = h_top[j] = 0u;
+    }
     if (a.post || (row_scale && a.x_q)) {
-        if (row_scale) top = lane_amax(x);
-        row_sum_max(ss, top, many, r, s_x);
-        if (a.post) {
-            post_rstd = inverse_rms(ss, a.H, a.inv_H, a.eps);
-            if (a.post_rstd && r.lane == 0) a.post_rstd[t] = post_rstd;
-        }
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                float x[W];
+                widen_piece<XT, W, END>(rx[j][u], r, r.piece(u), x);
+                ss[j] = ss[j] + tree_sumsq(x);
+                if (row_scale) x_top[j] = MaxBitsOp::f(x_top[j], own_amax<XT, W, END>(rx[j][u], r, r.piece(u), x));
+            }
+        if (row_scale)
+            rows_all<R, MANY, true>(ss, x_top, r, s_x);
+        else
+            rows_all<R, MANY, false>(ss, x_top, r, s_x);
+        if (a.post)
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                post_rstd[j] = inverse_rms(ss[j], a.H, a.inv_H, a.eps);
+                if (a.post_rstd && r.lane == 0 && first + j * a.rows < end) a.post_rstd[row(j)] = post_rstd[j];
+            }
     }
-    if constexpr (CK)
-        if (a.x_q) store_checkpoint<W, V, END>(a.x_q + t * a.H, a.x_scale + t * a.scales, a.block, a.q_dtype, r, top, x);
-    ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < R; ++j) ss[j] = 0.0f;
 #pragma unroll
     for (int u = 0; u < V; ++u) {
+        const int32_t i = r.piece(u);
         float c[W];
-        rv[u].template branch<END>(a.v, r, r.piece(u), c);
-        widen_piece<HT, W, END>(rr[u], r, r.piece(u), h[u]);
+        rv[u].template branch<END>(a.v, r, i, c);
 #pragma unroll
-        for (int e = 0; e < W; ++e) h[u][e] = fmaf(x[u][e] * post_rstd, c[e], a.residual_scale * h[u][e]);
-        rr[u].narrow(h[u]);  // taken as stored
-        rr[u].widen(h[u]);
-        if (END == kEnds && r.piece(u) >= r.full) {  // columns that are not its own: 0 * inf is NaN
-            const int32_t skip = r.skip(r.piece(u));
+        for (int j = 0; j < R; ++j) {
+            float x[W], h[W];
+            widen_piece<XT, W, END>(rx[j][u], r, i, x);
+            widen_piece<HT, W, END>(rr[j][u], r, i, h);
+            if constexpr (CK)
+                if (a.x_q && first + j * a.rows < end)
+                    store_checkpoint<W, END>(a.x_q + row(j) * a.H, a.x_scale + row(j) * a.scales, a.block, a.q_dtype, r, i,
+                                             row_scale ? x_top[j] : own_amax<XT, W, END>(rx[j][u], r, i, x), x);
 #pragma unroll
-            for (int e = 0; e < W; ++e) h[u][e] = e < skip ? 0.0f : h[u][e];
+            for (int e = 0; e < W; ++e) h[e] = fmaf(x[e] * post_rstd[j], c[e], a.residual_scale * h[e]);
+            if (END == kEnds && i >= r.full) {  // columns that are not its own: 0 * inf is NaN
+                const int32_t skip = r.skip(i);
+#pragma unroll
+                for (int e = 0; e < W; ++e) h[e] = e < skip ? 0.0f : h[e];
+            }
+            rr[j][u].narrow(h);  // taken as stored
+            rr[j][u].widen(h);
+            ss[j] = ss[j] + tree_sumsq(h);
+            if (row_scale) h_top[j] = MaxBitsOp::f(h_top[j], own_amax<HT, W, END>(rr[j][u], r, i, h));
         }
-        ss = ss + tree_sumsq(h[u]);
     }
-    top = row_scale ? lane_amax(h) : 0u;
-    row_sum_max(ss, top, many, r, s_h);
+    if (row_scale)
+        rows_all<R, MANY, true>(ss, h_top, r, s_h);
+    else
+        rows_all<R, MANY, false>(ss, h_top, r, s_h);
+    float rstd[R];
 #pragma unroll
-    for (int u = 0; u < V; ++u) store_values<HT, W, END>(out<HT>(a.h) + t * a.H, r, r.piece(u), h[u]);
-    if constexpr (CK)
-        if (a.h_q) store_checkpoint<W, V, END>(a.h_q + t * a.H, a.h_scale + t * a.scales, a.block, a.q_dtype, r, top, h);
-    if (!a.y) return;
-    const float rstd = inverse_rms(ss, a.H, a.inv_H, a.eps);
-    if (a.rstd && r.lane == 0) a.rstd[t] = rstd;
+    for (int j = 0; j < R; ++j) {
+        rstd[j] = inverse_rms(ss[j], a.H, a.inv_H, a.eps);
+        if (a.rstd && r.lane == 0 && first + j * a.rows < end) a.rstd[row(j)] = rstd[j];
+    }
 #pragma unroll
     for (int u = 0; u < V; ++u) {
+        const int32_t i = r.piece(u);
         float m[W];
-        rv[u].template multiplier<END>(a.v, r, r.piece(u), m);
+        if (a.y) rv[u].template multiplier<END>(a.v, r, i, m);
 #pragma unroll
-        for (int e = 0; e < W; ++e) h[u][e] = h[u][e] * rstd * m[e];
-        store_values<XT, W, END>(out<XT>(a.y) + t * a.H, r, r.piece(u), h[u]);
+        for (int j = 0; j < R; ++j) {
+            if (first + j * a.rows >= end) continue;
+            const int64_t t = row(j);
+            store_piece<HT, W, END>(out<HT>(a.h) + t * a.H, r, i, rr[j][u]);
+            float h[W];
+            rr[j][u].widen(h);
+            if constexpr (CK)
+                if (a.h_q)
+                    store_checkpoint<W, END>(a.h_q + t * a.H, a.h_scale + t * a.scales, a.block, a.q_dtype, r, i,
+                                             row_scale ? h_top[j] : own_amax<HT, W, END>(rr[j][u], r, i, h), h);
+            if (!a.y) continue;
+#pragma unroll
+            for (int e = 0; e < W; ++e) h[e] = h[e] * rstd[j] * m[e];
+            store_values<XT, W, END>(out<XT>(a.y) + t * a.H, r, i, h);
+        }
     }
 }
 
 template <typename XT, typename HT, int W>
-hipError_t fwd(const JoinArgs& a, const RowPlan& p, hipStream_t st)
+hipError_t fwd(const JoinArgs& a, bool several, int64_t grid, const RowPlan& p, hipStream_t st)
 {
-    const dim3 grid = dim3(unsigned((a.T + p.rows - 1) / p.rows));
     return with_row<W>(p, a.H, [&](auto v, auto end) {
-        constexpr int V = decltype(v)::value;
-        constexpr int E = decltype(end)::value;
-        return a.h_q || a.x_q ? launch(join_fwd_kernel<XT, HT, W, V, E, true>, grid, dim3(p.block), st, a)
-                              : launch(join_fwd_kernel<XT, HT, W, V, E, false>, grid, dim3(p.block), st, a);
+        constexpr int V = decltype(v)::value, E = decltype(end)::value, kRows = join_rows(V * W);
+        const auto go = [&](auto rows, auto many) {
+            constexpr int R = decltype(rows)::value;
+            constexpr bool M = decltype(many)::value;
+            return a.h_q || a.x_q
+                       ? launch(join_fwd_kernel<XT, HT, W, V, R, M, E, true>, dim3(unsigned(grid)), dim3(p.block), st, a)
+                       : launch(join_fwd_kernel<XT, HT, W, V, R, M, E, false>, dim3(unsigned(grid)), dim3(p.block), st, a);
+        };
+        const auto with = [&](auto many) {
+            if constexpr (kRows > 1)
+                if (several) return go(std::integral_constant<int, kRows>{}, many);
+            return go(std::integral_constant<int, 1>{}, many);
+        };
+        if constexpr (V == 1)
+            if (p.lanes <= 64) return with(std::false_type{});
+        if constexpr (E == kTiny)
+            return hipErrorInvalidValue;  // one lane, above
+        else
+            return with(std::true_type{});
     });
 }
 
@@ -162,33 +244,42 @@ template <typename XT, int W, int V, int END>
 __global__ void __launch_bounds__(kRowMaxBlock)
 quantize_kernel(QuantArgs a)
 {
-    __shared__ uint32_t s_top[2 * kRowMaxWaves];
+    __shared__ uint32_t s_top[kRowMaxWaves];
     const int32_t sub = a.lanes > 64 ? 0 : int32_t(threadIdx.x) / a.lanes;
     const Row<W> r = row_of<W>(a.H, a.lanes, int32_t(threadIdx.x) - sub * a.lanes);
     const int64_t t = int64_t(blockIdx.x) * a.rows + sub;
     if (t >= a.T) return;
-    float x[V][W];
     Piece<XT, W> rx[V];
     load_row<XT, W, V, END>(in<XT>(a.x) + t * a.x_stride, r, a.nt, rx);
+    uint32_t top[V];
+    float x[V][W];
 #pragma unroll
-    for (int u = 0; u < V; ++u) widen_piece<XT, W, END>(rx[u], r, r.piece(u), x[u]);
-    uint32_t top = 0;
-    if (a.block == 0) {
-        float unused = 0.0f;
-        top = lane_amax(x);
-        row_sum_max(unused, top, V > 1 || a.lanes > 64, r, s_top);
+    for (int u = 0; u < V; ++u) {
+        widen_piece<XT, W, END>(rx[u], r, r.piece(u), x[u]);
+        top[u] = own_amax<XT, W, END>(rx[u], r, r.piece(u), x[u]);
     }
-    store_checkpoint<W, V, END>(a.q + t * a.H, a.scale + t * a.scales, a.block, a.q_dtype, r, top, x);
+    if (a.block == 0) {
+#pragma unroll
+        for (int u = 1; u < V; ++u) top[0] = MaxBitsOp::f(top[0], top[u]);
+        top[0] = V > 1 || a.lanes > 64 ? row_all<MaxBitsOp, true>(top[0], r, s_top) : row_all<MaxBitsOp, false>(top[0], r, s_top);
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u)
+        store_checkpoint<W, END>(a.q + t * a.H, a.scale + t * a.scales, a.block, a.q_dtype, r, r.piece(u),
+                                 a.block ? top[u] : top[0], x[u]);
 }
 
 }  // namespace
 
-hipError_t launch_join_fwd(const JoinArgs& a, int x_dtype, int r_dtype, const RowPlan& p, hipStream_t st)
+hipError_t launch_join_fwd(const JoinArgs& a, int x_dtype, int r_dtype, bool several, int64_t grid, const RowPlan& p,
+                           hipStream_t st)
 {
-    if (x_dtype == GN_F32) return fwd<float, float, 4>(a, p, st);
+    if (x_dtype == GN_F32) return fwd<float, float, 4>(a, several, grid, p, st);
     if (r_dtype == GN_F32)
-        return x_dtype == GN_BF16 ? fwd<uint16_t, float, 4>(a, p, st) : fwd<_Float16, float, 4>(a, p, st);
-    return x_dtype == GN_BF16 ? fwd<uint16_t, uint16_t, 8>(a, p, st) : fwd<_Float16, _Float16, 8>(a, p, st);
+        return x_dtype == GN_BF16 ? fwd<uint16_t, float, 4>(a, several, grid, p, st)
+                                  : fwd<_Float16, float, 4>(a, several, grid, p, st);
+    return x_dtype == GN_BF16 ? fwd<uint16_t, uint16_t, 8>(a, several, grid, p, st)
+                              : fwd<_Float16, _Float16, 8>(a, several, grid, p, st);
 }
 
 hipError_t launch_q8_quantize(const QuantArgs& a, int x_dtype, const RowPlan& p, hipStream_t st)

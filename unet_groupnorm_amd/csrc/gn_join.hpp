@@ -36,15 +36,22 @@ struct JoinArgs {
     float* x_scale;
     JoinVecs v;
     int64_t T, H, x_stride;
-    int64_t first;    // the launch's first row
+    int64_t first;    // the launch's first workgroup
     int64_t len;      // rows of a sequence
+    int64_t groups;   // workgroups of a sequence; 0: any rows share one, each with vectors of its own
     int64_t scales;   // scales of a row of a checkpoint
     float eps, inv_H, residual_scale;
     int32_t lanes, rows;
     int32_t q_dtype, block;
-    bool post, one;   // the norm after the block; one sequence
+    bool post;        // the norm after the block
     bool nt;          // nontemporal loads of the rows
 };
+
+// Rows that a lane of the forward kernel takes one behind the other, by its columns of each. They
+// share the vectors, which are about half of its instructions. Fewer workgroups than
+// kJoinFill of several rows leave the chip idle: then each takes one.
+constexpr int32_t join_rows(int32_t columns) { return columns <= 8 ? 4 : columns <= 16 ? 2 : 1; }
+constexpr int64_t kJoinFill = 768;
 
 struct JoinBwdArgs {
     const void* dy;   // null: none
@@ -131,7 +138,8 @@ inline JoinPlan join_plan(int64_t T, int64_t H, int64_t samples, bool fp32)
     return p;
 }
 
-hipError_t launch_join_fwd(const JoinArgs& a, int x_dtype, int r_dtype, const RowPlan& p, hipStream_t st);
+hipError_t launch_join_fwd(const JoinArgs& a, int x_dtype, int r_dtype, bool several, int64_t grid, const RowPlan& p,
+                           hipStream_t st);
 
 // The gradients and partial sums in one kernel.
 hipError_t launch_join_bwd_16(const JoinBwdArgs& a, int x_dtype, const JoinPlan& p, hipStream_t st);

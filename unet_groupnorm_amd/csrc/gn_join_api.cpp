@@ -112,7 +112,6 @@ int gn::join_forward(const gn_join* j, const JoinForwardPtrs& p, void* stream, i
     a.v = vecs_of(j, w.p, post.p, gate.p, scale.p);
     a.H = H;
     a.x_stride = j->x_stride;
-    a.len = T / j->samples;
     a.scales = scales;
     a.eps = j->eps;
     a.inv_H = 1.0f / float(H);
@@ -122,22 +121,30 @@ int gn::join_forward(const gn_join* j, const JoinForwardPtrs& p, void* stream, i
     a.q_dtype = j->q_dtype;
     a.block = int32_t(j->block);
     a.post = j->post_norm != 0;
-    a.one = j->samples == 1 || (!gate.stride && !scale.stride);
+    a.T = T;
+    a.x = p.x;
+    a.res = p.residual;
+    a.h = p.h;
+    a.y = p.y;
+    a.rstd = rstd;
+    a.post_rstd = p.post_rstd;
+    a.h_q = static_cast<uint8_t*>(p.h_q);
+    a.x_q = static_cast<uint8_t*>(p.x_q);
+    a.h_scale = p.h_scale;
+    a.x_scale = p.x_scale;
     a.nt = T * H * (xs * (p.y ? 2 : 1) + 2 * rs + (p.h_q ? 1 : 0) + (p.x_q ? 1 : 0)) > gn::kRowStreamBytes;
-    for (int64_t t = 0; t < T; t += kMaxGroups * plan.rows) {
-        a.first = t;
-        a.T = std::min(T - t, kMaxGroups * plan.rows);
-        a.x = at(p.x, t * j->x_stride * xs);
-        a.res = at(p.residual, t * H * rs);
-        a.h = at(p.h, t * H * rs);
-        a.y = at(p.y, t * H * xs);
-        a.rstd = rstd ? rstd + t : nullptr;
-        a.post_rstd = p.post_rstd ? p.post_rstd + t : nullptr;
-        a.h_q = static_cast<uint8_t*>(at(p.h_q, t * H));
-        a.x_q = static_cast<uint8_t*>(at(p.x_q, t * H));
-        a.h_scale = p.h_scale ? p.h_scale + t * scales : nullptr;
-        a.x_scale = p.x_scale ? p.x_scale + t * scales : nullptr;
-        if (hipError_t e = gn::launch_join_fwd(a, j->x_dtype, j->r_dtype, plan, static_cast<hipStream_t>(stream)))
+    // one vector for all rows is one sequence
+    const int64_t sequences = gate.stride || scale.stride ? j->samples : 1;
+    a.len = T / sequences;
+    const int64_t at_once = int64_t(plan.rows) * gn::join_rows(plan.vecs * plan.width);
+    a.groups = (a.len + at_once - 1) / at_once;
+    const bool several = at_once > plan.rows && a.groups * sequences >= gn::kJoinFill;
+    if (!several) a.groups = a.len >= plan.rows ? (a.len + plan.rows - 1) / plan.rows : 0;
+    const int64_t grid = a.groups ? a.groups * sequences : (T + plan.rows - 1) / plan.rows;
+    for (int64_t k = 0; k < grid; k += kMaxGroups) {
+        a.first = k;
+        if (hipError_t e = gn::launch_join_fwd(a, j->x_dtype, j->r_dtype, several, std::min(grid - k, kMaxGroups), plan,
+                                               static_cast<hipStream_t>(stream)))
             return launch_status(e);
     }
     return GN_OK;

@@ -17,28 +17,43 @@ namespace gn {
 
 namespace {
 
-// Three sums over a row's lanes; with MANY lanes its waves meet in s (three words for each), and the
-// whole workgroup takes part.
+// A wave's sum in its last lane: within a row of 16 lanes as lanes_all, then from row to row. One
+// instruction a step; three sums in turn, so that none waits for itself.
+__device__ __forceinline__ void wave_sums(float (&v)[3])
+{
+    const auto step = [&](auto ctrl, auto mask) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            const int b = __builtin_amdgcn_update_dpp(0, __float_as_int(v[q]), decltype(ctrl)::value, decltype(mask)::value,
+                                                      0xF, decltype(mask)::value == 0xF);
+            v[q] = v[q] + __int_as_float(b);
+        }
+    };
+    using All = std::integral_constant<int, 0xF>;
+    step(std::integral_constant<int, 0xB1>{}, All{});
+    step(std::integral_constant<int, 0x4E>{}, All{});
+    step(std::integral_constant<int, 0x141>{}, All{});
+    step(std::integral_constant<int, 0x140>{}, All{});
+    step(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // rows 1 and 3 add rows 0 and 2
+    step(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // row 3 adds row 1's
+}
+
+// Three sums over a row's lanes; with MANY lanes its up to 8 waves meet in s, whose words of waves
+// that there are not are zero, and the whole workgroup takes part.
 template <bool MANY, int W>
-__device__ __forceinline__ void row_sums(float (&v)[3], const Row<W>& r, uint32_t* s)
+__device__ __forceinline__ void row_sums(float (&v)[3], const Row<W>& r, f32x4* s)
 {
     if (!MANY) {
 #pragma unroll
         for (int q = 0; q < 3; ++q) v[q] = __uint_as_float(lanes_all<AddOp>(__float_as_uint(v[q]), r.lanes));
         return;
     }
-    const int nw = r.lanes >> 6, k = r.lane & 7;  // 512 lanes at most
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        const uint32_t b = lanes_all<AddOp>(__float_as_uint(v[q]), 64);
-        if ((r.lane & 63) == 0) s[q * nw + (r.lane >> 6)] = b;
-    }
+    wave_sums(v);
+    if ((r.lane & 63) == 63) s[r.lane >> 6] = f32x4{v[0], v[1], v[2], 0.0f};
     __syncthreads();
+    const f32x4 w = s[r.lane & 7];
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        const uint32_t b = s[q * nw + (k < nw ? k : 0)];
-        v[q] = __uint_as_float(lanes_all<AddOp>(k < nw ? b : 0u, 8));
-    }
+    for (int q = 0; q < 3; ++q) v[q] = __uint_as_float(lanes_all<AddOp>(__float_as_uint(w[q]), 8));
 }
 
 // Keeps the compiler from moving what makes v behind what follows, or loads that follow in front of it.
@@ -93,14 +108,15 @@ struct Walk {
 // waits there. And a wait for those loads is not one for the stores behind them as long as no branch
 // leads round the stores: a group's rows behind the sequence's end, which are its last row once
 // more, store that row's bits once more (MANY; the barrier orders them behind the loads).
-template <typename XT, typename HT, bool CK, bool FULL, int W, int V, bool MANY, int END, bool NT>
+template <typename XT, typename HT, bool CK, bool FULL, int W, int V, bool MANY, int END, int DEPTH, bool NT>
 __global__ void __launch_bounds__(join_block(V * W))
 join_bwd_kernel(JoinBwdArgs a)
 {
     constexpr int E = END == kWhole ? kEnds : END;        // for loads and partial sums
     constexpr int kWiden = END == kWhole ? kExact : END;  // columns of others are wanted too
     constexpr int kBlock = join_block(V * W);
-    __shared__ uint32_t s_sum[2][3 * (kBlock / 64)];
+    constexpr int kSums = MANY ? kBlock / 128 * 8 : 1;  // 8 words for each of its rows
+    __shared__ f32x4 s_sum[2][kSums];
     __shared__ __align__(16) float s_part[kBlock * W];
     int32_t sub = int32_t(threadIdx.x) / a.lanes;
     if (MANY) sub = __builtin_amdgcn_readfirstlane(sub);
@@ -247,10 +263,14 @@ join_bwd_kernel(JoinBwdArgs a)
                 for (int k = 0; k < W; ++k) {
                     h[u][k] = h[u][k] * rstd;  // xhat
                     x[u][k] = x[u][k] * post_rstd;  // xpost
-                    if (live) A[u][k] = fmaf(dy[u][k], h[u][k], A[u][k]);
                     g[k] = dy[u][k] * m[u][k];
                     e[u][k] = fmaf(rstd, g[k], e[u][k]);
                     cx[k] = c[u][k] * x[u][k];
+                }
+                if (!MANY || live) {
+                    asm volatile("");  // a branch, not a choice for every element
+#pragma unroll
+                    for (int k = 0; k < W; ++k) A[u][k] = fmaf(dy[u][k], h[u][k], A[u][k]);
                 }
                 if (END == kWhole && r.piece(u) >= r.full) {
                     const int32_t skip = r.skip(r.piece(u));
@@ -265,7 +285,7 @@ join_bwd_kernel(JoinBwdArgs a)
                 v[2] = v[2] + tree_sumprod(h[u], cx);
             }
         }
-        row_sums<MANY>(v, r, s_sum[phase] + (MANY ? 3 * sub * (r.lanes >> 6) : 0));
+        row_sums<MANY>(v, r, s_sum[phase] + (MANY ? 8 * sub : 0));
         phase ^= 1;
         if (MANY || live) {  // behind the row's barrier
             const Row<W> q = again(r);
@@ -277,11 +297,13 @@ join_bwd_kernel(JoinBwdArgs a)
 #pragma unroll
                     for (int k = 0; k < W; ++k) e[u][k] = fmaf(-h[u][k], c1, e[u][k]);  // d
                 }
+                if (!MANY || live) {
+                    asm volatile("");
 #pragma unroll
-                for (int k = 0; k < W; ++k) {
-                    if (live) C[u][k] = fmaf(e[u][k], x[u][k], C[u][k]);
-                    o[k] = a.residual_scale * e[u][k];
+                    for (int k = 0; k < W; ++k) C[u][k] = fmaf(e[u][k], x[u][k], C[u][k]);
                 }
+#pragma unroll
+                for (int k = 0; k < W; ++k) o[k] = a.residual_scale * e[u][k];
                 if (has_dres) store(out<HT>(a.dres) + at, q, q.piece(u), o);
                 if (a.post) {
 #pragma unroll
@@ -311,23 +333,35 @@ join_bwd_kernel(JoinBwdArgs a)
             }
         }
     };
+    if (MANY) {
+        for (int32_t k = threadIdx.x; k < 2 * kSums; k += blockDim.x) (&s_sum[0][0])[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        __syncthreads();
+    }
     // The vectors first: behind the rows they would wait for those.
-    Loaded l;
+    Loaded l, l2;
     load_branch();
     if constexpr (V * W <= 8) {
         RawVec<W> more[2][V];
         load_multiplier(more);
         load(l);
+        if (DEPTH == 2) load(l2);
         take_branch();
         take_multiplier(more);
     } else {  // no registers for all at once
         take_branch();
         load_multiplier(rv);
         load(l);
+        if (DEPTH == 2) load(l2);
         take_multiplier(rv);
     }
     zero();
-    while (use.chunk < a.chunks) group(l);
+    while (use.chunk < a.chunks) {
+        group(l);
+        if (DEPTH == 2) {
+            if (use.chunk >= a.chunks) break;
+            group(l2);
+        }
+    }
 }
 
 template <typename XT, typename HT, int W, bool CK>
@@ -336,16 +370,16 @@ hipError_t one(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st)
     const dim3 grid = dim3(unsigned(p.grid)), block = dim3(p.block);
     const bool full = a.dy && a.dh && a.x && a.dx && a.dres;
     const auto go = [&](auto v, auto end) {
-        constexpr int V = decltype(v)::value, E = decltype(end)::value;
+        constexpr int V = decltype(v)::value, E = decltype(end)::value, kDepth = V * W <= 8 && E != kTiny ? 2 : 1;
         const auto with = [&](auto many) {
             constexpr bool M = decltype(many)::value;
-            if (!full) return launch(join_bwd_kernel<XT, HT, CK, false, W, V, M, E == kTiny ? kTiny : kEnds, false>, grid, block, st, a);
+            if (!full) return launch(join_bwd_kernel<XT, HT, CK, false, W, V, M, E == kTiny ? kTiny : kEnds, 1, false>, grid, block, st, a);
             // a shorter last piece may lie in two blocks of a checkpoint, whose scales its lane has not both
             if constexpr (CK && E == kWhole)
-                if (a.H % W && a.block) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, kEnds, false>, grid, block, st, a);
+                if (a.H % W && a.block) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, kEnds, 1, false>, grid, block, st, a);
             if constexpr (E == kExact)
-                if (a.nt) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, true>, grid, block, st, a);
-            return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, false>, grid, block, st, a);
+                if (a.nt) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, true>, grid, block, st, a);
+            return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, false>, grid, block, st, a);
         };
         if constexpr (V == 1)
             if (p.lanes <= 64) return with(std::false_type{});

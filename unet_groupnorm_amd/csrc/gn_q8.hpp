@@ -63,6 +63,21 @@ __device__ __forceinline__ uint32_t piece_amax(const float (&v)[W])
     return m;
 }
 
+// The same of a whole 16-bit piece as loaded: two elements' magnitude bits to an instruction.
+template <typename T, int W>
+__device__ __forceinline__ uint32_t piece_amax16(const Piece<T, W>& raw)
+{
+    typedef uint16_t Pair __attribute__((ext_vector_type(2)));
+    Pair m = {0, 0};
+#pragma unroll
+    for (int k = 0; k < W / 2; ++k) m = __builtin_elementwise_max(m, __builtin_bit_cast(Pair, raw.w[k] & 0x7fff7fffu));
+    const uint32_t top = m[0] > m[1] ? m[0] : m[1];
+    if constexpr (std::is_same<T, uint16_t>::value)
+        return top << 16;
+    else
+        return __float_as_uint(Io<_Float16>::lo(top));
+}
+
 // 4 quotients, at most an ulp above qmax in magnitude, to 4 bytes: nearest, ties to even. For
 // int8 1.5 * 2^23 is added, which leaves the integer in the sum's low bits. `zero` (a run that
 // holds a NaN or an infinity) makes them 0.
@@ -114,7 +129,8 @@ __device__ __forceinline__ void store_q8(uint8_t* q, float* scale, int32_t block
     const bool whole = END == kExact || i < r.full;
     store_q<W>(q + (whole ? i * W : r.column(i)), whole || END == kTiny ? 0 : W - r.tail,
                whole || END == kEnds ? W : r.H, v, sc, q_dtype);
-    if (block == 0 ? i == 0 : i % share == 0) scale[block == 0 ? 0 : i / share] = sc.scale;
+    // share is a power of two where block is not 0
+    if (block == 0 ? i == 0 : (i & (share - 1)) == 0) scale[block == 0 ? 0 : i >> (__ffs(share) - 1)] = sc.scale;
 }
 
 // Lanes that share a scale: the row's, or block / W neighbours (a row of fewer lanes than that

@@ -159,10 +159,12 @@ __device__ __forceinline__ void load_weight(const void* w, int dtype, const Row<
 
 // ------------------------------------------------------------------ sums over a row's lanes
 
+// The value of the lane that CTRL names; every lane has one, and the operation that takes it can be
+// one instruction with the exchange.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v)
 {
-    return uint32_t(__builtin_amdgcn_update_dpp(int(v), int(v), CTRL, 0xF, 0xF, false));
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, true));
 }
 
 struct AddOp {
