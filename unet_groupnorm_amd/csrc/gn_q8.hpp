@@ -151,10 +151,11 @@ __device__ __forceinline__ void widen_q8(const uint32_t (&b)[W / 4], int q_dtype
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[4 * k + e] = float(int8_t(b[k] >> (8 * e)));
         } else {
-            v[4 * k] = __builtin_amdgcn_cvt_f32_fp8(int(b[k]), 0);
-            v[4 * k + 1] = __builtin_amdgcn_cvt_f32_fp8(int(b[k]), 1);
-            v[4 * k + 2] = __builtin_amdgcn_cvt_f32_fp8(int(b[k]), 2);
-            v[4 * k + 3] = __builtin_amdgcn_cvt_f32_fp8(int(b[k]), 3);
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(b[k]), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(b[k]), true);
+            v[4 * k] = lo[0];
+            v[4 * k + 1] = lo[1];
+            v[4 * k + 2] = hi[0];
+            v[4 * k + 3] = hi[1];
         }
     }
 }

@@ -99,42 +99,74 @@ rms_fwd_kernel(RmsArgs a)
 
 // ------------------------------------------------------------------ values of the 8-bit form
 
-// A workgroup takes whole rows' pieces of W columns in turn (4 for an fp32 output, so that
-// its stores are 16 bytes a lane; 8 otherwise).
-template <typename OT, int W>
+// A thread takes 4 pieces of W columns (4 for an fp32 output, so that its stores are 16 bytes a lane;
+// 8 otherwise), whose loads are in flight together. Bound by its instructions until the integer
+// divisions went: FLAT (whole blocks in a row) takes a piece's scale by a shift of its place, the
+// others divide it by the row's pieces with a reciprocal, `inverse` = floor(2^32 / pieces), whose
+// quotient is the exact one or one less. total is below 2^31.
+template <typename OT, int W, bool FLAT>
 __global__ void __launch_bounds__(256)
-q8_dequantize_kernel(const uint8_t* q, int q_dtype, const float* scale, int64_t H, int64_t block, int64_t scales,
-                     OT* values, uint32_t pieces, uint64_t total)
+q8_dequantize_kernel(const uint8_t* q, int q_dtype, const float* scale, int32_t H, int32_t block, int32_t scales,
+                     OT* values, uint32_t pieces, uint32_t inverse, uint32_t total)
 {
-    const uint64_t step = uint64_t(gridDim.x) * 256;
-    for (uint64_t j = uint64_t(blockIdx.x) * 256 + threadIdx.x; j < total; j += step) {
-        const uint64_t t = total >> 32 ? j / pieces : uint64_t(uint32_t(j) / pieces);
-        const int64_t c = int64_t(j - t * pieces) * W, at = int64_t(t) * H + c;
-        const int n = H - c < W ? int(H - c) : W;
-        const float s = scale[int64_t(t) * scales + (block ? uint32_t(c) / uint32_t(block) : 0u)];
-        uint32_t b[W / 4];
-        if (n == W) {
-            typedef uint32_t WordsAny __attribute__((ext_vector_type(W / 4), aligned(1)));
-            const WordsAny x = *reinterpret_cast<const WordsAny*>(q + at);
+    constexpr int K = 4;
+    typedef uint32_t Words __attribute__((ext_vector_type(W / 4)));
+    typedef uint32_t WordsAny __attribute__((ext_vector_type(W / 4), aligned(1)));
+    const int32_t shift = block ? __ffs(block) - 1 : 0;
+    Words b[K];
+    float s[K];
+    int64_t at[K];
+    int n[K];
+    const uint32_t j0 = blockIdx.x * (256 * K) + threadIdx.x;
 #pragma unroll
-            for (int k = 0; k < W / 4; ++k) b[k] = x[k];
-        } else {
+    for (int k = 0; k < K; ++k) {
+        const uint32_t j = j0 + 256 * k;
+        n[k] = j < total ? W : 0;
+        if (FLAT) {
+            at[k] = int64_t(j) * W;
+            if (n[k]) {
+                b[k] = *reinterpret_cast<const WordsAny*>(q + at[k]);
+                s[k] = scale[at[k] >> shift];
+            }
+            continue;
+        }
+        uint32_t t = __umulhi(j, inverse), p = j - t * pieces;
+        if (p >= pieces) {
+            ++t;
+            p -= pieces;
+        }
+        const int32_t c = int32_t(p) * W;
+        at[k] = int64_t(t) * H + c;
+        if (n[k]) {
+            n[k] = H - c < W ? H - c : W;
+            s[k] = scale[int64_t(t) * scales + (c >> shift) * (block ? 1 : 0)];
+            if (n[k] == W) {
+                b[k] = *reinterpret_cast<const WordsAny*>(q + at[k]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                if ((e & 3) == 0) b[e / 4] = 0;
-                if (e < n) b[e / 4] |= uint32_t(q[at + e]) << (8 * (e & 3));
+                for (int e = 0; e < W; ++e) {
+                    if ((e & 3) == 0) b[k][e / 4] = 0;
+                    if (e < n[k]) b[k][e / 4] |= uint32_t(q[at[k] + e]) << (8 * (e & 3));
+                }
             }
         }
-        float v[W];
-        widen_q8(b, q_dtype, v);
+    }
 #pragma unroll
-        for (int e = 0; e < W; ++e) v[e] = v[e] * s;
+    for (int k = 0; k < K; ++k) {
+        if (!n[k]) continue;
+        uint32_t w[W / 4];
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i) w[i] = b[k][i];
+        float v[W];
+        widen_q8(w, q_dtype, v);
+#pragma unroll
+        for (int e = 0; e < W; ++e) v[e] = v[e] * s[k];
         Piece<OT, W> o;
         o.narrow(v);
-        if (n == W)
-            o.template store<false>(values + at);
+        if (FLAT || n[k] == W)
+            o.template store<false>(values + at[k]);
         else
-            o.store_part(values + at, n);
+            o.store_part(values + at[k], n[k]);
     }
 }
 
@@ -175,10 +207,20 @@ hipError_t launch_q8_dequantize(const void* q, int q_dtype, const float* scale, 
     return with_type(out_dtype, [&](auto t) {
         using OT = decltype(t);
         constexpr int W = sizeof(OT) == 4 ? 4 : 8;
-        const int64_t pieces = (H + W - 1) / W, total = T * pieces, scales = block ? (H + block - 1) / block : 1;
-        const int64_t grid = std::min<int64_t>((total + 255) / 256, int64_t(1) << 22);
-        return launch(q8_dequantize_kernel<OT, W>, dim3(unsigned(grid)), dim3(256), st, cp<uint8_t>(q), q_dtype, scale,
-                      H, block, scales, mp<OT>(values), uint32_t(pieces), uint64_t(total));
+        const int64_t pieces = (H + W - 1) / W, scales = block ? (H + block - 1) / block : 1;
+        const int64_t most = (int64_t(1) << 31) / pieces;  // rows of a launch
+        const uint32_t inverse = uint32_t(std::min<uint64_t>((uint64_t(1) << 32) / uint64_t(pieces), 0xffffffffu));
+        for (int64_t t = 0; t < T; t += most) {
+            const int64_t rows = std::min(most, T - t), total = rows * pieces;
+            const auto go = [&](auto kernel) {
+                return launch(kernel, dim3(unsigned((total + 1023) / 1024)), dim3(256), st, cp<uint8_t>(q) + t * H, q_dtype,
+                              scale + t * scales, int32_t(H), int32_t(block), int32_t(scales), mp<OT>(values) + t * H,
+                              uint32_t(pieces), inverse, uint32_t(total));
+            };
+            const bool flat = block ? H % block == 0 : false;
+            if (hipError_t e = flat ? go(q8_dequantize_kernel<OT, W, true>) : go(q8_dequantize_kernel<OT, W, false>)) return e;
+        }
+        return hipSuccess;
     });
 }
 
