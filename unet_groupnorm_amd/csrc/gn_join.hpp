@@ -48,9 +48,11 @@ struct JoinArgs {
 };
 
 // Rows that a lane of the forward kernel takes one behind the other, by its columns of each. They
-// share the vectors, which are about half of its instructions. Fewer workgroups than
-// kJoinFill of several rows leave the chip idle: then each takes one.
-constexpr int32_t join_rows(int32_t columns) { return columns <= 8 ? 4 : columns <= 16 ? 2 : 1; }
+// share the vectors, which are about a third of its instructions. Measured with 1, 2 and 4 rows (2
+// where a lane has 16 columns): 4096 x 1152 bf16 with a gate and a scale of each image 12.7, 11.8, 12.5
+// us; 8192 x 4096 bf16 51.0 with one and 50.8 with 2. Fewer workgroups than kJoinFill (3 for each CU)
+// of several rows leave the chip idle: then each takes one.
+constexpr int32_t join_rows(int32_t columns) { return columns <= 16 ? 2 : 1; }
 constexpr int64_t kJoinFill = 768;
 
 struct JoinBwdArgs {
@@ -165,6 +167,10 @@ struct JoinVecGrads {
     int64_t H, chunks, split, samples;
 };
 hipError_t launch_join_vectors(const JoinVecGrads& a, hipStream_t st);
+
+// Calls that move more than this many bytes load nontemporally: a 128^3 x 32 bf16 activation (192 MiB with
+// its 8 bits) to int8 and back 64.1 us so, 69.5 otherwise.
+constexpr int64_t kQuantStreamBytes = int64_t(128) << 20;
 
 struct QuantArgs {
     const void* x;

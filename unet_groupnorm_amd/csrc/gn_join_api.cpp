@@ -287,7 +287,7 @@ int gn::q8_quantize(const void* x, int x_dtype, int64_t x_stride, int64_t T, int
     a.rows = p.rows;
     a.q_dtype = q_dtype;
     a.block = int32_t(block);
-    a.nt = T * H * (size_of(x_dtype) + 1) > gn::kRowStreamBytes;
+    a.nt = T * H * (size_of(x_dtype) + 1) > gn::kQuantStreamBytes;
     for (int64_t t = 0; t < T; t += kMaxGroups * p.rows) {
         a.T = std::min(T - t, kMaxGroups * p.rows);
         a.x = at(x, t * x_stride * size_of(x_dtype));
