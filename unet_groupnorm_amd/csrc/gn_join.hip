@@ -7,7 +7,10 @@
 //
 // A row is read once into registers, reduced there twice (x for the norm after the block, h for
 // the norm before the next one, which is of the rounded sum and so cannot be had from the same
-// pass), and written once.
+// pass), and written once. Bound by the bytes it moves: bf16, 8192 x 4096 with a gate: 47 us, 5.7
+// TB/s (the row norm, with one reduction and one vector: 41.7); with int8 checkpoints of both, 64 us,
+// 5.2 TB/s, where the rounding to 8 bits comes to half the instructions. Smaller rows are bound by
+// their instructions: 4096 x 1152 with a gate and a scale of each of 16 images 11.5 us, 3.3 TB/s.
 #include "gn_join_vec.hpp"
 
 namespace gn {
@@ -77,7 +80,7 @@ __device__ __forceinline__ void store_checkpoint(uint8_t* q, float* scale, int32
 // the second reduction's barrier: they may take an input's place, and lanes at the row's end read
 // columns of others. CK: checkpoints may be asked for. MANY: rows of more than 64 lanes, one place.
 template <typename XT, typename HT, int W, int V, int R, bool MANY, int END, bool CK>
-__global__ void __launch_bounds__(kRowMaxBlock)
+__global__ void __launch_bounds__(join_fwd_block(V, R))
 join_fwd_kernel(JoinArgs a)
 {
     __shared__ uint32_t s_x[MANY ? R : 1][2 * kRowMaxWaves], s_h[MANY ? R : 1][2 * kRowMaxWaves];
@@ -101,7 +104,8 @@ join_fwd_kernel(JoinArgs a)
     };
     Piece<XT, W> rx[R][V];
     Piece<HT, W> rr[R][V];
-    RawVecs<W> rv[V];
+    constexpr bool kLate = V * W > 16;  // no registers for the vectors beside the rows: loaded piece by piece
+    RawVecs<W> rv[kLate ? 1 : V];
     if (a.nt) {
         asm volatile("" ::: "memory");
 #pragma unroll
@@ -118,7 +122,8 @@ join_fwd_kernel(JoinArgs a)
         }
     }
 #pragma unroll
-    for (int u = 0; u < V; ++u) rv[u].template load<END>(a.v, n, r, r.piece(u));
+    for (int u = 0; u < V; ++u)
+        if (!kLate) rv[u].template load<END>(a.v, n, r, r.piece(u));
     const bool row_scale = CK && a.block == 0;
     float ss[R], post_rstd[R];
     uint32_t x_top[R], h_top[R];
@@ -155,7 +160,9 @@ join_fwd_kernel(JoinArgs a)
     for (int u = 0; u < V; ++u) {
         const int32_t i = r.piece(u);
         float c[W];
-        rv[u].template branch<END>(a.v, r, i, c);
+        RawVecs<W>& q = rv[kLate ? 0 : u];
+        if (kLate) q.template load<END>(a.v, n, r, i);
+        q.template branch<END>(a.v, r, i, c);
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             float x[W], h[W];
@@ -192,7 +199,9 @@ join_fwd_kernel(JoinArgs a)
     for (int u = 0; u < V; ++u) {
         const int32_t i = r.piece(u);
         float m[W];
-        if (a.y) rv[u].template multiplier<END>(a.v, r, i, m);
+        RawVecs<W>& q = rv[kLate ? 0 : u];
+        if (kLate) q.template load<END>(a.v, n, r, i);
+        if (a.y) q.template multiplier<END>(a.v, r, i, m);
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             if (first + j * a.rows >= end) continue;
@@ -272,7 +281,7 @@ quantize_kernel(QuantArgs a)
 // Rows of whole blocks one behind the other are a list of blocks: no row, no end of one. A thread takes
 // 4 pieces, whose loads are in flight together; a block's lanes are neighbours in a wave. total counts
 // pieces and is a multiple of a block's, as are a workgroup's. For the general kernel a 128^3 x 32
-// activation in blocks of 128 takes 40 us, for this one 33.
+// activation in blocks of 128 takes 40 us, for this one 33 (6.1 TB/s).
 template <typename XT, int W, bool NT>
 __global__ void __launch_bounds__(256)
 quantize_blocks_kernel(const XT* x, uint8_t* q, float* scale, int32_t q_dtype, int32_t share, int64_t total)

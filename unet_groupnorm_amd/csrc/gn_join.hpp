@@ -54,6 +54,9 @@ struct JoinArgs {
 // of several rows leave the chip idle: then each takes one.
 constexpr int32_t join_rows(int32_t columns) { return columns <= 16 ? 2 : 1; }
 constexpr int64_t kJoinFill = 768;
+// Threads of the largest workgroup of a forward kernel: with fewer a lane has the registers that two
+// rows of 16 columns take (with 128 of them 9 go to scratch memory and back, a quarter more bytes).
+constexpr int32_t join_fwd_block(int32_t pieces, int32_t rows) { return pieces == 1 ? 256 : rows > 1 ? 512 : kRowMaxBlock; }
 
 struct JoinBwdArgs {
     const void* dy;   // null: none

@@ -1,6 +1,8 @@
-// gn_join_wide.hip -- backward of the residual join over rows too wide for a workgroup's registers, in
-// two kernels: the rows' means, then the gradients and the sums over rows, columns by columns
-// (gn_join_bwd.hpp has the formulas); and the vectors' gradients from the partial sums of both.
+// gn_join_wide.hip -- backward of the residual join over rows too wide for a workgroup's registers (past
+// 8192 columns), in two kernels: the rows' means, then the gradients and the sums over rows, columns by
+// columns (gn_join_bwd.hpp has the formulas). So the rows are read twice: 2730 x 12288 bf16 142 us, 1170
+// x 28672 162, where one reading takes 60. And the vectors' gradients from the partial sums of both
+// ways.
 #include "gn_join_vec.hpp"
 
 namespace gn {
@@ -226,7 +228,7 @@ __device__ __forceinline__ void partials4(const JoinVecGrads& a, int64_t p, int6
 // A workgroup adds 32 columns of the partial sums, a thread 4 columns. The first `tiles` workgroups
 // add all sequences' chunks, a thread those at slice, slice + 128, ...; the others take `per`
 // sequences each (where the gate or the scale is a vector for each), a thread the chunks at its place
-// within one. Bound by trips to memory, not by bytes. Sums of A and of C, and weighted by the
+// within one. Bound by trips to memory, not by bytes: 4.5 to 6 us. Sums of A and of C, and weighted by the
 // sequences' vectors where those differ.
 __global__ void __launch_bounds__(kVecBlock)
 join_vectors_kernel(JoinVecGrads a, int64_t first, uint32_t tiles, int32_t per)
