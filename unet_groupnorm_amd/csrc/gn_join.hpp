@@ -117,13 +117,16 @@ inline int64_t join_split(int64_t groups, int64_t samples)
     return split;
 }
 
-// Threads of the backward's workgroup, by the columns of a lane.
+// Threads of the backward's workgroup, by the columns of a lane: as many as leave each its registers. Of
+// 8 columns with 512, 768 and 1024 threads: 4096 x 1152 bf16 24.7, 23.7, 40.5 us, 513 x 1001 fp32 13.4, 12.8,
+// 13.3.
 constexpr int32_t join_block(int32_t columns) { return columns <= 8 ? 768 : kBwdBlock; }
 
 inline JoinPlan join_plan(int64_t T, int64_t H, int64_t samples, bool fp32)
 {
     JoinPlan p;
     static_cast<RowPlan&>(p) = row_plan(H, fp32, true);
+    // one piece a lane up to 512 lanes: 8192 x 4096 bf16 73.1 us, with two on 256 lanes 77.3
     if (p.width == 8 && p.vecs == 2 && H <= 4096) {
         p.vecs = 1;
         p.lanes = int32_t(((H + 7) / 8 + 63) / 64 * 64);

@@ -108,14 +108,14 @@ struct Walk {
 // more than 64). The next group's loads are in flight behind the one in use. Every lane keeps its
 // columns' vectors and sums in registers; at a chunk's end the workgroup adds its rows' sums in LDS
 // and leaves two partial sums for each column. FULL: dy, dh, h, x, dx and dres are all there; else
-// each may be missing, behind branches. NT: nontemporal loads.
+// each may be missing, behind branches. NT: nontemporal loads (8192 x 4096 bf16: 75 us, without 86).
 //
 // A group's values are widened before the next group is loaded into the registers that they came in
 // (pin): otherwise the compiler loads into others and copies them at the loop's end, for which it
 // waits there. And a wait for those loads is not one for the stores behind them as long as no branch
 // leads round the stores: a group's rows behind the sequence's end, which are its last row once
 // more, store that row's bits once more (MANY; the barrier orders them behind the loads).
-template <typename XT, typename HT, bool CK, bool FULL, int W, int V, bool MANY, int END, int DEPTH, bool NT>
+template <typename XT, typename HT, bool CK, bool FULL, int W, int V, bool MANY, int END, bool NT>
 __global__ void __launch_bounds__(join_block(V * W))
 join_bwd_kernel(JoinBwdArgs a)
 {
@@ -345,30 +345,22 @@ join_bwd_kernel(JoinBwdArgs a)
         __syncthreads();
     }
     // The vectors first: behind the rows they would wait for those.
-    Loaded l, l2;
+    Loaded l;
     load_branch();
     if constexpr (V * W <= 8) {
         RawVec<W> more[2][V];
         load_multiplier(more);
         load(l);
-        if (DEPTH == 2) load(l2);
         take_branch();
         take_multiplier(more);
     } else {  // no registers for all at once
         take_branch();
         load_multiplier(rv);
         load(l);
-        if (DEPTH == 2) load(l2);
         take_multiplier(rv);
     }
     zero();
-    while (use.chunk < a.chunks) {
-        group(l);
-        if (DEPTH == 2) {
-            if (use.chunk >= a.chunks) break;
-            group(l2);
-        }
-    }
+    while (use.chunk < a.chunks) group(l);
 }
 
 template <typename XT, typename HT, int W, bool CK>
@@ -377,16 +369,16 @@ hipError_t one(const JoinBwdArgs& a, const JoinPlan& p, hipStream_t st)
     const dim3 grid = dim3(unsigned(p.grid)), block = dim3(p.block);
     const bool full = a.dy && a.dh && a.x && a.dx && a.dres;
     const auto go = [&](auto v, auto end) {
-        constexpr int V = decltype(v)::value, E = decltype(end)::value, kDepth = V * W <= 8 && E != kTiny ? 2 : 1;
+        constexpr int V = decltype(v)::value, E = decltype(end)::value;
         const auto with = [&](auto many) {
             constexpr bool M = decltype(many)::value;
-            if (!full) return launch(join_bwd_kernel<XT, HT, CK, false, W, V, M, E == kTiny ? kTiny : kEnds, 1, false>, grid, block, st, a);
+            if (!full) return launch(join_bwd_kernel<XT, HT, CK, false, W, V, M, E == kTiny ? kTiny : kEnds, false>, grid, block, st, a);
             // a shorter last piece may lie in two blocks of a checkpoint, whose scales its lane has not both
             if constexpr (CK && E == kWhole)
-                if (a.H % W && a.block) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, kEnds, 1, false>, grid, block, st, a);
+                if (a.H % W && a.block) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, kEnds, false>, grid, block, st, a);
             if constexpr (E == kExact)
-                if (a.nt) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, true>, grid, block, st, a);
-            return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, kDepth, false>, grid, block, st, a);
+                if (a.nt) return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, true>, grid, block, st, a);
+            return launch(join_bwd_kernel<XT, HT, CK, true, W, V, M, E, false>, grid, block, st, a);
         };
         if constexpr (V == 1)
             if (p.lanes <= 64) return with(std::false_type{});
